@@ -17,6 +17,10 @@ Entry points (same names as the C ABI):
   ``spec_verify_sample_lmhead``: the same from the target's hidden states and
   LM head (logits formed on the matrix cores, never written)
 * ``spec_commit_tree_kv``, ``spec_ngram_candidates``, ``sv_read_probe``
+* over a paged cache (``PagedKV``): ``spec_append_kv_paged`` (norms, rotation
+  and cache write of a window), ``spec_attend_paged`` (its attention),
+  ``spec_commit_tree_kv_paged``
+* ``spec_token_logprobs`` (log probabilities, entropy, alternatives)
 """
 
 from __future__ import annotations
@@ -31,18 +35,23 @@ LIB_PATH = os.environ.get("SPECVERIFY_LIB") or os.path.join(HERE, "libspecverify
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_WORKSPACE, SV_ERR_HIP, SV_ERR_SCRATCH = range(6)
 SV_NOALLOC_SCRATCH_BYTES = 8 << 20
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_E4M3 = 0, 1, 2
 SV_MAX_TREE_NODES = 2048
+SV_MAX_WINDOW = 64
+SV_MAX_TOP = 32
 KERNELS = ("rowstats", "accept", "resid_mass", "resid_select", "argmax", "match", "tree",
            "skip_stats", "skip_argmax", "commit", "lmhead", "ngram_count", "ngram_emit",
-           "skip_tree", "read_probe", "lmhead_stats", "lmhead_rows", "merge_parts")
+           "skip_tree", "read_probe", "lmhead_stats", "lmhead_rows", "merge_parts",
+           "append_paged", "attend", "attend_join", "commit_paged", "logprob", "logprob_merge")
 
 EXPORTS = ("sv_sample_workspace_bytes", "sv_greedy_workspace_bytes", "spec_verify_sample",
            "spec_verify_greedy", "spec_verify_tree", "spec_commit_tree_kv", "sv_status_string",
            "sv_version", "sv_lmhead_workspace_bytes", "spec_verify_greedy_lmhead",
            "spec_verify_tree_lmhead", "sv_ngram_workspace_bytes", "spec_ngram_candidates",
            "sv_read_probe", "sv_read_probe_folds", "sv_trace_begin", "sv_trace_end", "sv_kernel_name",
-           "sv_sample_lmhead_workspace_bytes", "spec_verify_sample_lmhead", "spec_verify_sample_noalloc")
+           "sv_sample_lmhead_workspace_bytes", "spec_verify_sample_lmhead", "spec_verify_sample_noalloc",
+           "spec_append_kv_paged", "sv_attend_workspace_bytes", "spec_attend_paged", "spec_commit_tree_kv_paged",
+           "sv_token_logprobs_workspace_bytes", "spec_token_logprobs")
 
 
 class SpecVerifyError(RuntimeError):
@@ -53,6 +62,12 @@ class SpecVerifyError(RuntimeError):
 
 class KernelTime(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("ms", ctypes.c_float)]
+
+
+class _PagedKVStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dt", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
 _lib = None
@@ -96,6 +111,19 @@ def load_library(path: str = LIB_PATH):
     lib.spec_verify_sample_lmhead.argtypes = [P, P, P, P, P, P, I, I, I, I, I, ctypes.c_float, P, P, P, P,
                                               P, P, Z, P]
     lib.spec_verify_sample_lmhead.restype = I
+    L, F, KV = ctypes.c_longlong, ctypes.c_float, _PagedKVStruct
+    lib.spec_append_kv_paged.argtypes = [P, P, P, L, L, L, P, P, F, P, I, I, I, P, P, P, I, I, I, KV, P, I, P, P, P]
+    lib.spec_append_kv_paged.restype = I
+    lib.sv_attend_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    lib.sv_attend_workspace_bytes.restype = Z
+    lib.spec_attend_paged.argtypes = [P, L, KV, P, I, P, P, P, I, I, I, F, P, P, P, P, Z, P]
+    lib.spec_attend_paged.restype = I
+    lib.spec_commit_tree_kv_paged.argtypes = [P, P, I, I, I, I, I, P, I, I, P, P, P, P, I, P, P]
+    lib.spec_commit_tree_kv_paged.restype = I
+    lib.sv_token_logprobs_workspace_bytes.argtypes = [I, I, I, I]
+    lib.sv_token_logprobs_workspace_bytes.restype = Z
+    lib.spec_token_logprobs.argtypes = [P, P, I, I, I, F, I, P, P, P, P, P, P, Z, P]
+    lib.spec_token_logprobs.restype = I
     lib.sv_read_probe.argtypes = [P, Z, P, P]
     lib.sv_read_probe.restype = I
     lib.sv_read_probe_folds.argtypes = [Z]
@@ -550,6 +578,259 @@ def spec_commit_tree_kv(kv, tree_base, commit_base, accept_len, path, *, out=Non
         raise SpecVerifyError(rc, "spec_commit_tree_kv")
     _hold(torch, dev, stream, st)
     return st
+
+
+# ---- paged cache -----------------------------------------------------------------
+
+class PagedKV:
+    """One layer's paged KV cache: the arrays a program keeps, checked once.
+
+    k_pages and v_pages [num_pages, kv_heads, page_size, head_dim], contiguous, bfloat16
+    or float8_e4m3fn; the latter with k_scales and v_scales [num_pages, kv_heads,
+    page_size] float32.  page_size a power of two in [16, 1024], head_dim 64, 128
+    or 256.  The arrays may be slices of one allocation (``kv[layer, 0]``)."""
+
+    def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
+        import torch
+
+        _check(k_pages, "k_pages", 4)
+        _check(v_pages, "v_pages", 4, k_pages.dtype, k_pages.device)
+        if tuple(v_pages.shape) != tuple(k_pages.shape):
+            raise ValueError("v_pages must have the shape of k_pages")
+        if k_pages.dtype == torch.bfloat16:
+            dt = SV_BF16
+            if k_scales is not None or v_scales is not None:
+                raise ValueError("a bfloat16 cache has no scales")
+        elif k_pages.dtype == torch.float8_e4m3fn:
+            dt = SV_E4M3
+            for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
+                _check(s, name, 3, torch.float32, k_pages.device)
+                if tuple(s.shape) != tuple(k_pages.shape[:3]):
+                    raise ValueError(f"{name} must be {list(k_pages.shape[:3])}")
+        else:
+            raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self.device = k_pages.device
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k_pages.shape
+        self._c = _PagedKVStruct(k_pages.data_ptr(), v_pages.data_ptr(),
+                                 None if k_scales is None else k_scales.data_ptr(),
+                                 None if v_scales is None else v_scales.data_ptr(), dt, self.num_pages,
+                                 self.kv_heads, self.page_size, self.head_dim)
+
+
+def _window_rows(torch, t, name, heads, head_dim, dev, lead=None):
+    """[B, N, heads, head_dim] bf16 whose heads are consecutive and whose tokens are
+    equally far apart (a slice of a projection's output); returns that distance."""
+    if t is None or t.dim() != 4:
+        raise ValueError(f"{name} must be [B, N, heads, head_dim]")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    B, N, H, D = t.shape
+    if D != head_dim or (heads is not None and H != heads) or (lead is not None and (B, N) != lead):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}")
+    sb, sn, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be consecutive")
+    if N == 1:
+        return sb if B > 1 else H * D
+    if B > 1 and sb != N * sn:
+        raise ValueError(f"{name}: tokens must be equally far apart")
+    return sn
+
+
+def _window_ints(torch, t, name, shape, dev):
+    if t is None:
+        return
+    _check(t, name, len(shape), torch.int32, dev)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+
+
+def _window_out(torch, t, name, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check(t, name, len(shape), dtype, dev)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t
+
+
+def spec_append_kv_paged(q, k, v, cache, page_table, base, positions=None, *, q_weight=None, k_weight=None,
+                         eps=1e-6, rope=None, interleaved=False, counts=None, q_out=None, status=True,
+                         stream=None):
+    """Write a window's keys and values into ``cache`` (a PagedKV), with the
+    per-head norms (q_weight, k_weight [head_dim] bf16) and the rotation (rope
+    [max_pos, rot] float32: rot/2 cosines, rot/2 sines; positions [B, N] int32) of
+    queries and keys in the same pass.
+
+    q [B, N, H, head_dim], k and v [B, N, kv_heads, head_dim] bf16, each a
+    contiguous tensor or a slice of a projection's output; page_table [B, P],
+    base [B] (cached tokens before the window), counts [B] (rows in use) int32.
+    Returns ``q`` [B, N, H, head_dim] bf16 (``q_out`` if given; rows behind counts
+    are left as they were) and ``status`` [B, N]."""
+    torch = _torch()
+    lib = load_library()
+    dev, D = cache.device, cache.head_dim
+    qs = _window_rows(torch, q, "q", None, D, dev)
+    B, N, H, _ = q.shape
+    ks = _window_rows(torch, k, "k", cache.kv_heads, D, dev, (B, N))
+    vs = _window_rows(torch, v, "v", cache.kv_heads, D, dev, (B, N))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check(w, name, 1, torch.bfloat16, dev)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must be [{D}]")
+    rot = max_pos = 0
+    if rope is not None:
+        _check(rope, "rope", 2, torch.float32, dev)
+        max_pos, rot = rope.shape
+        if positions is None:
+            raise ValueError("positions is required with rope")
+    _window_ints(torch, positions, "positions", (B, N), dev)
+    _check(page_table, "page_table", 2, torch.int32, dev)
+    if page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, P]")
+    _check(base, "base", 1, torch.int32, dev)
+    _window_ints(torch, base, "base", (B,), dev)
+    _window_ints(torch, counts, "counts", (B,), dev)
+    out = dict(q=_window_out(torch, q_out, "q_out", (B, N, H, D), torch.bfloat16, dev))
+    if status:
+        out["status"] = torch.empty((B, N), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        rc = lib.spec_append_kv_paged(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_weight), _ptr(k_weight), float(eps),
+            _ptr(rope), rot, max_pos, int(bool(interleaved)), _ptr(positions), base.data_ptr(), _ptr(counts),
+            B, N, H, cache._c, page_table.data_ptr(), page_table.shape[1], out["q"].data_ptr(),
+            _ptr(out.get("status")), _stream(torch, dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_append_kv_paged")
+    _hold(torch, dev, stream, *out.values())
+    return out
+
+
+def attend_workspace_bytes(B, N, H, kv_heads, head_dim, P, page_size) -> int:
+    return int(load_library().sv_attend_workspace_bytes(B, N, H, kv_heads, head_dim, P, page_size))
+
+
+def spec_attend_paged(q, cache, page_table, base, *, parents=None, counts=None, scale=None, out=None,
+                      lse=False, status=True, workspace=None, stream=None):
+    """Attention of a window's rows over ``cache`` (a PagedKV that already holds
+    the window's own keys and values): one new token, a draft chain, or with
+    ``parents`` [B, N] int32 a draft tree.
+
+    q [B, N, H, head_dim] bf16, N <= 64; page_table [B, P], base [B], counts [B]
+    int32; scale defaults to head_dim ** -0.5.  Returns ``out`` [B, N, H,
+    head_dim] bf16, ``lse`` [B, N, H] float32 (lse=True, or a tensor to write)
+    and ``status`` [B].  Rows behind counts are left as they were in ``out`` and
+    ``lse``."""
+    torch = _torch()
+    lib = load_library()
+    dev, D = cache.device, cache.head_dim
+    qs = _window_rows(torch, q, "q", None, D, dev)
+    B, N, H, _ = q.shape
+    _check(page_table, "page_table", 2, torch.int32, dev)
+    if page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, P]")
+    P = page_table.shape[1]
+    _check(base, "base", 1, torch.int32, dev)
+    _window_ints(torch, base, "base", (B,), dev)
+    _window_ints(torch, counts, "counts", (B,), dev)
+    _window_ints(torch, parents, "parents", (B, N), dev)
+    res = dict(out=_window_out(torch, out, "out", (B, N, H, D), torch.bfloat16, dev))
+    if lse is not False and lse is not None:
+        res["lse"] = _window_out(torch, None if lse is True else lse, "lse", (B, N, H), torch.float32, dev)
+    if status:
+        res["status"] = torch.empty(B, dtype=torch.int32, device=dev)
+    ws = _workspace(torch, lib.sv_attend_workspace_bytes(B, N, H, cache.kv_heads, D, P, cache.page_size), dev,
+                    workspace)
+    with torch.cuda.device(dev):
+        rc = lib.spec_attend_paged(
+            q.data_ptr(), qs, cache._c, page_table.data_ptr(), P, base.data_ptr(), _ptr(counts), _ptr(parents),
+            B, N, H, float(D ** -0.5 if scale is None else scale), res["out"].data_ptr(), _ptr(res.get("lse")),
+            _ptr(res.get("status")), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(torch, dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_attend_paged")
+    _hold(torch, dev, stream, ws if workspace is None else None, *res.values())
+    return res
+
+
+def spec_commit_tree_kv_paged(pages, page_table, tree_base, commit_base, accept_len, path, *, scales=None,
+                              status=True, stream=None):
+    """spec_commit_tree_kv inside a paged cache, in place: pages [G, num_pages,
+    kv_heads, page_size, head_dim] (any dtype; rows of 16 * 2^i bytes up to 1024),
+    scales [G, num_pages, kv_heads, page_size] float32 moved with the rows,
+    page_table [B, P], tree_base, commit_base, accept_len [B] and path [B, N]
+    int32.  Returns the per-request status [B] (or None)."""
+    torch = _torch()
+    lib = load_library()
+    _check(pages, "pages", 5)
+    dev = pages.device
+    G, num_pages, kv_heads, page_size, D = pages.shape
+    if scales is not None:
+        _check(scales, "scales", 4, torch.float32, dev)
+        if tuple(scales.shape) != tuple(pages.shape[:4]):
+            raise ValueError(f"scales must be {list(pages.shape[:4])}")
+    _check(page_table, "page_table", 2, torch.int32, dev)
+    B, P = page_table.shape
+    for name, t in (("tree_base", tree_base), ("commit_base", commit_base), ("accept_len", accept_len)):
+        _check(t, name, 1, torch.int32, dev)
+        if t.shape[0] != B:
+            raise ValueError(f"{name} must be [B]")
+    _check(path, "path", 2, torch.int32, dev)
+    if path.shape[0] != B:
+        raise ValueError("path must be [B, N]")
+    st = torch.empty(B, dtype=torch.int32, device=dev) if status else None
+    with torch.cuda.device(dev):
+        rc = lib.spec_commit_tree_kv_paged(
+            pages.data_ptr(), _ptr(scales), G, num_pages, kv_heads, page_size, D * pages.element_size(),
+            page_table.data_ptr(), P, B, tree_base.data_ptr(), commit_base.data_ptr(), accept_len.data_ptr(),
+            path.data_ptr(), path.shape[1], _ptr(st), _stream(torch, dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_commit_tree_kv_paged")
+    _hold(torch, dev, stream, st)
+    return st
+
+
+def token_logprobs_workspace_bytes(R, V, dtype_code, top_k) -> int:
+    return int(load_library().sv_token_logprobs_workspace_bytes(R, V, dtype_code, top_k))
+
+
+def spec_token_logprobs(logits, tokens=None, *, temperature=1.0, top_k=0, entropy=True, status=True,
+                        workspace=None, stream=None):
+    """Log probabilities under softmax(logits / temperature): logits [R, V] (bf16
+    or f32, contiguous), tokens [R] int32 (a row whose token is -1 is not read).
+    Returns ``logprob`` [R] (with tokens), ``entropy`` [R] in nats, ``top_ids`` and
+    ``top_logprobs`` [R, top_k] (top_k <= 32, by falling probability, ties to the
+    lowest id) and ``status`` [R]."""
+    torch = _torch()
+    lib = load_library()
+    _check(logits, "logits", 2)
+    dev = logits.device
+    R, V = logits.shape
+    dt = _dtype_code(logits)
+    _window_ints(torch, tokens, "tokens", (R,), dev)
+    out = {}
+    if tokens is not None:
+        out["logprob"] = torch.empty(R, dtype=torch.float32, device=dev)
+    if entropy:
+        out["entropy"] = torch.empty(R, dtype=torch.float32, device=dev)
+    if top_k:
+        out["top_ids"] = torch.empty((R, max(top_k, 0)), dtype=torch.int32, device=dev)
+        out["top_logprobs"] = torch.empty((R, max(top_k, 0)), dtype=torch.float32, device=dev)
+    if status:
+        out["status"] = torch.empty(R, dtype=torch.int32, device=dev)
+    ws = _workspace(torch, lib.sv_token_logprobs_workspace_bytes(R, V, dt, top_k), dev, workspace)
+    with torch.cuda.device(dev):
+        rc = lib.spec_token_logprobs(
+            logits.data_ptr(), _ptr(tokens), R, V, dt, float(temperature), top_k, _ptr(out.get("logprob")),
+            _ptr(out.get("entropy")), _ptr(out.get("top_ids")), _ptr(out.get("top_logprobs")),
+            _ptr(out.get("status")), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(torch, dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_token_logprobs")
+    _hold(torch, dev, stream, ws if workspace is None else None, *out.values())
+    return out
 
 
 def sv_read_probe(buf, *, folds=None, stream=None):

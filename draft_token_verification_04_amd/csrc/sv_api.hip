@@ -655,6 +655,263 @@ sv_status spec_commit_tree_kv(const void *src_kv, void *dst_kv, int G, int B, in
     return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
+}  // extern "C"
+
+// ---- paged cache ---------------------------------------------------------------------
+
+namespace {
+
+bool power_of_two(int x) { return x > 0 && (x & (x - 1)) == 0; }
+
+bool paged_sizes_ok(int page_size, int head_dim) {
+    return power_of_two(page_size) && page_size >= 16 && page_size <= 1024 &&
+           (head_dim == 64 || head_dim == 128 || head_dim == 256);
+}
+
+// The cache's own fields and the table's size.
+sv_status check_cache(const sv_paged_kv &c, int P) {
+    if (c.dt != SV_BF16 && c.dt != SV_E4M3) return SV_ERR_UNSUPPORTED;
+    if (c.num_pages < 1 || c.kv_heads < 1 || c.page_size < 1 || c.head_dim < 1 || P < 1) return SV_ERR_INVALID_ARG;
+    if (!paged_sizes_ok(c.page_size, c.head_dim) || static_cast<long long>(P) * c.page_size > 0x7fffffffLL)
+        return SV_ERR_UNSUPPORTED;
+    const double bytes = static_cast<double>(c.num_pages) * c.kv_heads * c.page_size * c.head_dim;
+    if (bytes >= 4.0e18) return SV_ERR_UNSUPPORTED;
+    return SV_OK;
+}
+sv_status check_cache_pointers(const sv_paged_kv &c) {
+    if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v)) return SV_ERR_INVALID_ARG;
+    if (c.dt == SV_E4M3 && (!c.k_scale || !c.v_scale || !aligned16(c.k_scale) || !aligned16(c.v_scale)))
+        return SV_ERR_INVALID_ARG;
+    return SV_OK;
+}
+
+bool attend_sizes_ok(int B, int N, int H, int kv_heads, int head_dim, int P, int page_size) {
+    if (!paged_sizes_ok(page_size, head_dim) || static_cast<long long>(P) * page_size > 0x7fffffffLL) return false;
+    if (N > SV_MAX_WINDOW || H > 65536 || static_cast<double>(B) * N * H > 2.0e9) return false;
+    if (B == 0) return true;
+    const AttendPlan p = attend_plan(B, N, H, kv_heads, head_dim, P, page_size);
+    // workgroups of the grid, rounded up to whole octets
+    return (static_cast<double>(p.S) * B * kv_heads + 8.0) * p.QB < 2147483647.0;
+}
+
+}  // namespace
+
+extern "C" {
+
+sv_status spec_append_kv_paged(const void *q, const void *k, const void *v, long long q_stride,
+                               long long k_stride, long long v_stride, const void *q_weight,
+                               const void *k_weight, float eps, const float *rope, int rot, int max_pos,
+                               int interleaved, const int32_t *positions, const int32_t *base,
+                               const int32_t *counts, int B, int N, int H, sv_paged_kv cache,
+                               const int32_t *page_table, int P, void *q_out, int32_t *token_status,
+                               hipStream_t stream) {
+    sv_status st = check_cache(cache, P);
+    if (st != SV_OK) return st;
+    if (B < 0 || N < 1 || H < 1 || !(eps >= 0.0f) || !isfinite(eps)) return SV_ERR_INVALID_ARG;
+    const int D = cache.head_dim;
+    if (rope) {
+        if (rot < 1 || rot > D || max_pos < 1) return SV_ERR_INVALID_ARG;
+        if (rot % 16 != 0) return SV_ERR_UNSUPPORTED;
+    }
+    if (static_cast<long long>(B) * N > 0x7fffffffLL || static_cast<long long>(H) + 2LL * cache.kv_heads > 65536)
+        return SV_ERR_UNSUPPORTED;
+    if (B == 0) return SV_OK;
+    if (!q || !k || !v || !base || !page_table || !q_out || (rope && !positions)) return SV_ERR_INVALID_ARG;
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return SV_ERR_INVALID_ARG;
+    st = check_cache_pointers(cache);
+    if (st != SV_OK) return st;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope) ||
+        !aligned16(q_weight) || !aligned16(k_weight))
+        return SV_ERR_INVALID_ARG;
+    const long long least[3] = {static_cast<long long>(H) * D, static_cast<long long>(cache.kv_heads) * D,
+                                static_cast<long long>(cache.kv_heads) * D};
+    const long long strides[3] = {q_stride, k_stride, v_stride};
+    for (int i = 0; i < 3; ++i) {
+        if (strides[i] % 8 != 0 || (strides[i] < least[i] && static_cast<long long>(B) * N > 1))
+            return SV_ERR_INVALID_ARG;
+        if (strides[i] > 1LL << 31) return SV_ERR_UNSUPPORTED;
+    }
+    AppendArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_weight = static_cast<const uint16_t *>(q_weight);
+    a.k_weight = static_cast<const uint16_t *>(k_weight);
+    a.eps = eps;
+    a.rope = rope;
+    a.rot = rope ? rot : 0;
+    a.max_pos = max_pos;
+    a.interleaved = interleaved != 0;
+    a.positions = positions;
+    a.base = base;
+    a.counts = counts;
+    a.page_table = page_table;
+    a.N = N;
+    a.H = H;
+    a.Hkv = cache.kv_heads;
+    a.P = P;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(cache.page_size));
+    a.num_pages = cache.num_pages;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.k_pages = cache.k;
+    a.v_pages = cache.v;
+    a.k_scale = cache.k_scale;
+    a.v_scale = cache.v_scale;
+    a.status = token_status;
+    const hipError_t e = traced(SV_K_APPEND_PAGED, stream,
+                                [&] { return launch_append(a, D, cache.dt == SV_E4M3, B * N, stream); });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+size_t sv_attend_workspace_bytes(int B, int N, int H, int kv_heads, int head_dim, int P, int page_size) {
+    if (B < 1 || N < 1 || H < 1 || kv_heads < 1 || P < 1 || H % kv_heads != 0 ||
+        !attend_sizes_ok(B, N, H, kv_heads, head_dim, P, page_size))
+        return 0;
+    return std::max<size_t>(256, attend_plan(B, N, H, kv_heads, head_dim, P, page_size).total);
+}
+
+sv_status spec_attend_paged(const void *q, long long q_stride, sv_paged_kv cache, const int32_t *page_table,
+                            int P, const int32_t *base, const int32_t *counts, const int32_t *parents, int B,
+                            int N, int H, float scale, void *out, float *lse, int32_t *req_status,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    sv_status st = check_cache(cache, P);
+    if (st != SV_OK) return st;
+    if (B < 0 || N < 1 || H < 1 || H % cache.kv_heads != 0 || !(scale > 0.0f) || !isfinite(scale))
+        return SV_ERR_INVALID_ARG;
+    const int D = cache.head_dim;
+    if (!attend_sizes_ok(B, N, H, cache.kv_heads, D, P, cache.page_size)) return SV_ERR_UNSUPPORTED;
+    if (B == 0) return SV_OK;
+    if (!q || !page_table || !base || !out || !workspace) return SV_ERR_INVALID_ARG;
+    st = check_cache_pointers(cache);
+    if (st != SV_OK) return st;
+    if (!aligned16(q) || !aligned16(out) || !aligned256(workspace)) return SV_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || (q_stride < static_cast<long long>(H) * D && static_cast<long long>(B) * N > 1))
+        return SV_ERR_INVALID_ARG;
+    if (q_stride > 1LL << 31) return SV_ERR_UNSUPPORTED;
+    const AttendPlan p = attend_plan(B, N, H, cache.kv_heads, D, P, cache.page_size);
+    if (workspace_bytes < std::max<size_t>(256, p.total)) return SV_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    AttendArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.q_stride = q_stride;
+    a.k_pages = cache.k;
+    a.v_pages = cache.v;
+    a.k_scale = cache.k_scale;
+    a.v_scale = cache.v_scale;
+    a.page_table = page_table;
+    a.base = base;
+    a.counts = counts;
+    a.parents = parents;
+    a.B = B;
+    a.N = N;
+    a.H = H;
+    a.Hkv = cache.kv_heads;
+    a.G = H / cache.kv_heads;
+    a.P = P;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(cache.page_size));
+    a.num_pages = cache.num_pages;
+    a.scale = scale;
+    a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634073599246810018921);
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.status = req_status;
+    a.S = p.S;
+    a.QB = p.QB;
+    a.min_tiles = p.min_tiles;
+    a.part_o = reinterpret_cast<float *>(ws + p.part_o);
+    a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
+    a.part_bad = reinterpret_cast<int32_t *>(ws + p.part_bad);
+    if (!isfinite(a.c)) return SV_ERR_UNSUPPORTED;
+    const bool e4m3 = cache.dt == SV_E4M3;
+    hipError_t e = traced(SV_K_ATTEND, stream, [&] { return launch_attend(a, D, e4m3, p.QT, stream); });
+    if (e == hipSuccess && p.S > 1)
+        e = traced(SV_K_ATTEND_JOIN, stream, [&] { return launch_attend_join(a, D, p.QT, stream); });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+sv_status spec_commit_tree_kv_paged(void *pages, float *scales, int G, int num_pages, int kv_heads,
+                                    int page_size, int row_bytes, const int32_t *page_table, int P, int B,
+                                    const int32_t *tree_base, const int32_t *commit_base,
+                                    const int32_t *accept_len, const int32_t *path_nodes, int N,
+                                    int32_t *req_status, hipStream_t stream) {
+    if (G < 1 || B < 0 || num_pages < 1 || kv_heads < 1 || P < 1 || N < 1 || page_size < 1 || row_bytes < 16 ||
+        row_bytes % 16 != 0)
+        return SV_ERR_INVALID_ARG;
+    if (!power_of_two(page_size) || page_size < 16 || page_size > 1024 || !power_of_two(row_bytes) ||
+        row_bytes > 1024 || N > SV_MAX_TREE_NODES || static_cast<long long>(P) * page_size > 0x7fffffffLL ||
+        static_cast<double>(G) * B * kv_heads > 2.0e9)
+        return SV_ERR_UNSUPPORTED;
+    if (static_cast<double>(G) * num_pages * kv_heads * page_size * row_bytes >= 9.0e18) return SV_ERR_UNSUPPORTED;
+    if (B == 0) return SV_OK;
+    if (!pages || !page_table || !tree_base || !commit_base || !accept_len || !path_nodes) return SV_ERR_INVALID_ARG;
+    if (!aligned16(pages)) return SV_ERR_INVALID_ARG;
+    const hipError_t e = traced(SV_K_COMMIT_PAGED, stream, [&] {
+        return launch_commit_paged(pages, scales, G, B, kv_heads, num_pages,
+                                   __builtin_ctz(static_cast<unsigned>(page_size)), row_bytes / 16, page_table, P,
+                                   tree_base, commit_base, accept_len, path_nodes, N, req_status, stream);
+    });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+}  // extern "C"
+
+// ---- log probabilities ---------------------------------------------------------------
+
+namespace {
+struct LogprobWs {
+    size_t keys, total;
+};
+LogprobWs logprob_ws_layout(int R, int V, sv_dtype dt, int k) {
+    const size_t n = static_cast<size_t>(R) * static_cast<size_t>(logprob_segs(R, V, dt));
+    LogprobWs w;
+    w.keys = align_up(n * sizeof(LogprobPart));
+    w.total = w.keys + align_up(n * static_cast<size_t>(k) * sizeof(uint64_t));
+    return w;
+}
+}  // namespace
+
+extern "C" {
+
+size_t sv_token_logprobs_workspace_bytes(int R, int V, sv_dtype dt, int top_k) {
+    if (R < 1 || !valid_dtype(dt) || top_k < 0 || top_k > SV_MAX_TOP || top_k > V || !sizes_ok(R, 1, V)) return 0;
+    return logprob_ws_layout(R, V, dt, top_k).total;
+}
+
+sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, int V, sv_dtype dt,
+                              float temperature, int top_k, float *logprob, float *entropy,
+                              int32_t *top_ids, float *top_logprobs, int32_t *row_status, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+    if (!valid_dtype(dt)) return SV_ERR_UNSUPPORTED;
+    if (R < 0 || V < 1 || top_k < 0 || top_k > V || !(temperature > 0.0f) || !isfinite(temperature))
+        return SV_ERR_INVALID_ARG;
+    if (top_k > SV_MAX_TOP || !sizes_ok(R, 1, V)) return SV_ERR_UNSUPPORTED;
+    if (R == 0) return SV_OK;
+    if (!logits || !workspace || !aligned256(workspace) || (logprob && !tokens) ||
+        (top_k > 0 && (!top_ids || !top_logprobs)))
+        return SV_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % (dt == SV_BF16 ? 2 : 4) != 0) return SV_ERR_INVALID_ARG;
+    const double c = 1.4426950408889634073599246810018921 / static_cast<double>(temperature);
+    const int segs = logprob_segs(R, V, dt);
+    if (!(c < 0x1p127) || static_cast<double>(R) * segs > 8.0e9) return SV_ERR_UNSUPPORTED;
+    const LogprobWs L = logprob_ws_layout(R, V, dt, top_k);
+    if (workspace_bytes < L.total) return SV_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    const LogprobArgs a = {logits, tokens, R, V, segs, top_k, static_cast<float>(c),
+                           reinterpret_cast<LogprobPart *>(ws), reinterpret_cast<uint64_t *>(ws + L.keys),
+                           logprob, entropy, top_ids, top_logprobs, row_status};
+    hipError_t e = traced(SV_K_LOGPROB, stream, [&] { return launch_logprob(a, dt, stream); });
+    if (e == hipSuccess)
+        e = traced(SV_K_LOGPROB_MERGE, stream, [&] { return launch_logprob_merge(a, dt, stream); });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+}  // extern "C"
+
+extern "C" {
+
 size_t sv_read_probe_folds(size_t bytes) {
     return static_cast<size_t>(read_probe_waves(static_cast<long long>(bytes / 16)));
 }
@@ -691,7 +948,8 @@ const char *sv_kernel_name(int k) {
                                             "argmax", "match", "tree", "skip_stats",
                                             "skip_argmax", "commit", "lmhead", "ngram_count",
                                             "ngram_emit", "skip_tree", "read_probe", "lmhead_stats",
-                                            "lmhead_rows", "merge_parts"};
+                                            "lmhead_rows", "merge_parts", "append_paged", "attend",
+                                            "attend_join", "commit_paged", "logprob", "logprob_merge"};
     return (k >= 0 && k < SV_K_COUNT) ? names[k] : "unknown";
 }
 

@@ -110,6 +110,95 @@ __global__ __launch_bounds__(kBlock) void k_commit(const uint4 *src, uint4 *dst,
         copy_rows<true>(from, into, d * row_vecs, row_vecs, p0, path, lane);
 }
 
+// ---- the same inside a paged cache ---------------------------------------------------
+//
+// A slot of request b lies in page page_table[b][slot / page_size], where each
+// head's rows are consecutive.  One wave per (array g, request b, head): rows
+// of different heads never meet, so the order argument above holds per wave.
+// Lane i of a group of kWave path nodes looks up node i's source and
+// destination row once; the copy then reads them from that lane.
+
+// Row of `slot` in a head's arrays (in units of rows), or -1 for a slot outside
+// the table or a page outside the cache.
+__device__ __forceinline__ long long paged_row(const int32_t *__restrict__ pages, int P, int page_shift,
+                                               int num_pages, int Hkv, int h, long long slot) {
+    if (slot < 0 || (slot >> page_shift) >= P) return -1;
+    const int page = pages[slot >> page_shift];
+    if (page < 0 || page >= num_pages) return -1;
+    return ((static_cast<long long>(page) * Hkv + h) << page_shift) + (slot & ((1 << page_shift) - 1));
+}
+
+__global__ __launch_bounds__(kBlock) void k_commit_paged(
+    uint4 *pages, float *scales, int G, int B, int Hkv, int num_pages, int page_shift, int vec_shift,
+    const int32_t *__restrict__ page_table, int P, const int32_t *__restrict__ tree_base,
+    const int32_t *__restrict__ commit_base, const int32_t *__restrict__ accept_len,
+    const int32_t *__restrict__ path_nodes, int N, int32_t *__restrict__ status) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const long long wave = static_cast<long long>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6);
+    if (wave >= static_cast<long long>(G) * B * Hkv) return;
+    const int h = static_cast<int>(wave % Hkv);
+    const long long gb = wave / Hkv;
+    const int b = static_cast<int>(gb % B), g = static_cast<int>(gb / B);
+    const int32_t *path = path_nodes + static_cast<long long>(b) * N;
+    const int32_t *table = page_table + static_cast<long long>(b) * P;
+    const int d = uniform(accept_len[b]);
+    const long long tb = uniform(tree_base[b]), cb = uniform(commit_base[b]);
+
+    // request check (every wave of the request reaches the same verdict)
+    int code = 0;
+    if (d < 0 || d > N - 1) {
+        code = 2;
+    } else if (d > 0) {
+        bool bad = false, out = false;
+        for (int k = lane; k < d; k += kWave) {
+            const int j = path[k];
+            const int prev = k == 0 ? 0 : path[k - 1];
+            if (j < 1 || j >= N || j <= prev)
+                bad = true;
+            else if (paged_row(table, P, page_shift, num_pages, Hkv, 0, tb + j) < 0)
+                out = true;
+            if (paged_row(table, P, page_shift, num_pages, Hkv, 0, cb + k) < 0) out = true;
+        }
+        if (ballot(bad) != 0)
+            code = 2;
+        else if (ballot(out) != 0)
+            code = 1;
+        else if (cb >= tb + 2 && cb < tb + N)
+            code = 3;
+    }
+    if (g == 0 && h == 0 && lane == 0 && status) status[b] = code;
+    if (code != 0 || d == 0) return;
+
+    const long long rows = (static_cast<long long>(num_pages) * Hkv) << page_shift;  // rows of one array
+    uint4 *base = pages + ((static_cast<long long>(g) * rows) << vec_shift);
+    float *sbase = scales ? scales + static_cast<long long>(g) * rows : nullptr;
+    const int rows_per = kWave >> vec_shift;  // rows one instruction of the wave moves
+    const int sub = lane >> vec_shift, v = lane & ((1 << vec_shift) - 1);
+    for (int k0 = 0; k0 < d; k0 += kWave) {
+        const int nk = min(kWave, d - k0), k = min(lane, nk - 1) + k0;
+        const long long src = paged_row(table, P, page_shift, num_pages, Hkv, h, tb + path[k]);
+        const long long dst = paged_row(table, P, page_shift, num_pages, Hkv, h, cb + k);
+        float sc = 0.0f;
+        if (sbase) sc = sbase[src];
+        for (int r0 = 0; r0 < nk; r0 += rows_per * kCommitVecs) {
+            uint4 x[kCommitVecs];
+#pragma unroll
+            for (int t = 0; t < kCommitVecs; ++t) {
+                const int r = min(r0 + t * rows_per + sub, nk - 1);
+                x[t] = base[(__shfl(src, r, kWave) << vec_shift) + v];
+            }
+            wait_own_stores();  // every load of the chunk has returned before any store
+#pragma unroll
+            for (int t = 0; t < kCommitVecs; ++t) {
+                const int r = r0 + t * rows_per + sub;
+                const long long to = __shfl(dst, min(r, nk - 1), kWave);
+                if (r < nk) base[(to << vec_shift) + v] = x[t];
+            }
+        }
+        if (sbase && lane < nk) sbase[dst] = sc;
+    }
+}
+
 }  // namespace
 
 hipError_t launch_commit(const void *src, void *dst, int G, int B, int S, int row_bytes,
@@ -122,6 +211,18 @@ hipError_t launch_commit(const void *src, void *dst, int G, int B, int S, int ro
                          static_cast<const uint4 *>(src), static_cast<uint4 *>(dst), G, B,
                          static_cast<long long>(S), row_bytes / 16, tree_base, commit_base, accept_len,
                          path_nodes, N, src == dst ? 1 : 0, status);
+}
+
+hipError_t launch_commit_paged(void *pages, float *scales, int G, int B, int Hkv, int num_pages, int page_shift,
+                               int vecs, const int32_t *page_table, int P, const int32_t *tree_base,
+                               const int32_t *commit_base, const int32_t *accept_len, const int32_t *path_nodes,
+                               int N, int32_t *status, hipStream_t s) {
+    const long long waves = static_cast<long long>(G) * B * Hkv;
+    const long long blocks = (waves + kWavesPerBlock - 1) / kWavesPerBlock;
+    return launch_kernel(k_commit_paged, dim3(static_cast<unsigned>(blocks)), dim3(kBlock), 0, s,
+                         static_cast<uint4 *>(pages), scales, G, B, Hkv, num_pages, page_shift,
+                         __builtin_ctz(static_cast<unsigned>(vecs)), page_table, P, tree_base, commit_base,
+                         accept_len, path_nodes, N, status);
 }
 
 }  // namespace sv

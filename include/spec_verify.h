@@ -77,6 +77,7 @@ typedef enum {
 typedef enum {
     SV_F32 = 0,
     SV_BF16 = 1,
+    SV_E4M3 = 2, /* 8-bit floats (e4m3, no infinities): elements of a paged cache only */
     SV_DTYPE_MIN_ENUM = -0x7fffffff - 1, /* not dtypes: the type spans every int */
     SV_DTYPE_MAX_ENUM = 0x7fffffff
 } sv_dtype;
@@ -343,6 +344,146 @@ sv_status spec_ngram_candidates(const int32_t *context, int B, int L, const int3
                                 size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * A paged KV cache (passed by value; its pointers are device pointers).
+ *   k, v  [num_pages][kv_heads][page_size][head_dim] elements of dtype dt
+ *         (SV_BF16 or SV_E4M3), 16-byte aligned.
+ *   k_scale, v_scale  for SV_E4M3: [num_pages][kv_heads][page_size] float32, the
+ *         factor of each row's elements, 16-byte aligned; NULL for SV_BF16.
+ *   page_size a power of two in [16, 1024], head_dim 64, 128 or 256 (else
+ *   SV_ERR_UNSUPPORTED), num_pages and kv_heads at least 1.
+ * Slot s of request b is row s % page_size of page page_table[b][s / page_size],
+ * page_table [B][P] int32 on the device.  Page ids are checked before they are
+ * used as addresses.  P * page_size must be below 2^31 (else
+ * SV_ERR_UNSUPPORTED); offsets into the cache are 64-bit.
+ *
+ * A request's cached tokens fill its slots from 0; a window of N new tokens
+ * (one token, a draft chain, or the nodes of a draft tree) takes the slots
+ * base[b], base[b] + 1, ...  counts [B] (int32, may be NULL: N) gives the
+ * window's rows in use, clipped to [0, N]; what belongs to the rows behind
+ * them is left as it was.
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    sv_dtype dt;
+    int num_pages, kv_heads, page_size, head_dim;
+} sv_paged_kv;
+
+/* Largest window spec_attend_paged accepts. */
+#define SV_MAX_WINDOW 64
+/* Most alternatives per row spec_token_logprobs returns. */
+#define SV_MAX_TOP 32
+
+/*
+ * Writes a window's keys and values into a paged cache, with the per-head norms
+ * and the position rotation of queries and keys in the same pass (what the
+ * target's pass over prefix and drafts does before its attention).
+ *
+ *   q [B][N] rows of H heads, k and v [B][N] rows of kv_heads heads, head_dim
+ *     bf16 values each, heads consecutive; token t = b N + n starts at
+ *     t * stride elements (q_stride, k_stride, v_stride: multiples of 8, so
+ *     that the three may be slices of one projection's output).  16-byte
+ *     aligned.
+ *   q_weight, k_weight  [head_dim] bf16, 16-byte aligned, or both NULL (no
+ *     norm): y = x / sqrt(mean(x^2) + eps) * weight, eps >= 0.
+ *   rope  [max_pos][rot] float32, 16-byte aligned, or NULL (no rotation): rot/2
+ *     cosines, then rot/2 sines of the position's angles.  rot a multiple of 16
+ *     in [16, head_dim].  Pair i of the first rot values of a head, values
+ *     (i, i + rot/2), or (2i, 2i + 1) with interleaved != 0, becomes
+ *     (a cos_i - b sin_i, b cos_i + a sin_i).
+ *   positions [B][N] int32 (may be NULL without rope), base [B], counts [B].
+ *   q_out [B][N][H][head_dim] bf16, contiguous, 16-byte aligned.
+ *   token_status [B][N] optional: 0; 1 the slot is outside the table, or its
+ *     page outside the cache; 2 the position is outside [0, max_pos).  A token
+ *     with a non-zero status, or behind counts, writes nothing.
+ * Everything is computed in fp32 and rounded once, to nearest even.  An e4m3
+ * row is stored as round(y * (448 / a)) with scale a / 448, a = max |y| (a row
+ * of zeros: scale 0).  A row that holds an infinity or NaN is stored so that it
+ * reads back as NaN where it was not finite.
+ * Two tokens that share a slot race; the slots of a window are distinct.
+ */
+sv_status spec_append_kv_paged(const void *q, const void *k, const void *v, long long q_stride,
+                               long long k_stride, long long v_stride, const void *q_weight,
+                               const void *k_weight, float eps, const float *rope, int rot, int max_pos,
+                               int interleaved, const int32_t *positions, const int32_t *base,
+                               const int32_t *counts, int B, int N, int H, sv_paged_kv cache,
+                               const int32_t *page_table, int P, void *q_out, int32_t *token_status,
+                               hipStream_t stream);
+
+/*
+ * Attention of a window's rows over a paged cache that already holds the
+ * window's own keys and values (spec_append_kv_paged): one new token (N = 1), a
+ * draft chain, or a draft tree.
+ *
+ *   q [B][N] rows of H heads of head_dim bf16 values, as above (q_stride).  H a
+ *     multiple of kv_heads: query head i reads KV head i / (H / kv_heads).
+ *   parents [B][N] int32 as for spec_verify_tree (parents[b][0] = -1,
+ *     0 <= parents[b][j] < j), or NULL for a chain.  Row n sees every slot below
+ *     base[b], its own, and those of its ancestors (chain: of the rows before it).
+ *   1 <= N <= SV_MAX_WINDOW, scale > 0 finite.
+ *   out [B][N][H][head_dim] bf16 = softmax(scale q k^T) v over the slots seen,
+ *     16-byte aligned; lse [B][N][H] float32, optional: the log of the sum of
+ *     exp(scale q k^T) over them.
+ *   req_status [B] optional: 0; 1 a slot is outside the table (or base[b] < 0), or a
+ *     page outside the cache; 2 the parent array is malformed.  The rows of a
+ *     request with a non-zero status are 0, their lse -inf.
+ * Weights are rounded to bf16 for the second product; sums and maxima are fp32.
+ * What a masked slot holds, infinities and NaN included, reaches no row.
+ * Workspace: sv_attend_workspace_bytes (0 for invalid or unsupported sizes).
+ */
+size_t sv_attend_workspace_bytes(int B, int N, int H, int kv_heads, int head_dim, int P, int page_size);
+
+sv_status spec_attend_paged(const void *q, long long q_stride, sv_paged_kv cache, const int32_t *page_table,
+                            int P, const int32_t *base, const int32_t *counts, const int32_t *parents, int B,
+                            int N, int H, float scale, void *out, float *lse, int32_t *req_status,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * spec_commit_tree_kv inside a paged cache: the rows of each request's accepted
+ * path move, in place, into consecutive slots.
+ *
+ *   pages  [G][num_pages][kv_heads][page_size] rows of row_bytes bytes, 16-byte
+ *          aligned; row_bytes 16 times a power of two, at most 1024.  G counts
+ *          the arrays that share the page table (layers x {K, V}).
+ *   scales [G][num_pages][kv_heads][page_size] float32 moved with the rows, or
+ *          NULL.
+ *   page_table [B][P], tree_base, commit_base, accept_len, path_nodes [B][N]
+ *          and req_status (optional) as for spec_commit_tree_kv; status 1 also
+ *          for a page outside the cache.  Requests must not share the pages
+ *          they write.
+ */
+sv_status spec_commit_tree_kv_paged(void *pages, float *scales, int G, int num_pages, int kv_heads,
+                                    int page_size, int row_bytes, const int32_t *page_table, int P, int B,
+                                    const int32_t *tree_base, const int32_t *commit_base,
+                                    const int32_t *accept_len, const int32_t *path_nodes, int N,
+                                    int32_t *req_status, hipStream_t stream);
+
+/*
+ * Log probabilities of given tokens under softmax(logits / temperature), the
+ * entropy of each row, and its top_k most probable tokens (what a server
+ * reports beside the tokens that verification emitted).
+ *
+ *   logits [R][V] of dtype dt (SV_F32 or SV_BF16; any alignment of the element
+ *          type), tokens [R] int32 or NULL.
+ *   0 <= top_k <= SV_MAX_TOP, top_k <= V.
+ *   logprob [R] (optional; needs tokens), entropy [R] (optional, in nats),
+ *   top_ids [R][top_k] int32 by falling probability, equal logits by rising id,
+ *   top_logprobs [R][top_k] (NULL when top_k = 0).
+ *   row_status [R] optional: 0, or 1 if the token is outside [0, V) (its
+ *          logprob is then -inf).
+ * A row whose token is -1, what verification pads out_tokens with, is not read:
+ * its logprob and entropy are 0, its ids -1 and their logprobs -inf.  Logits of
+ * -inf have probability 0; a row of nothing else has entropy 0.
+ * Workspace: sv_token_logprobs_workspace_bytes (0 for invalid sizes).
+ */
+size_t sv_token_logprobs_workspace_bytes(int R, int V, sv_dtype dt, int top_k);
+
+sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, int V, sv_dtype dt,
+                              float temperature, int top_k, float *logprob, float *entropy,
+                              int32_t *top_ids, float *top_logprobs, int32_t *row_status, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Measurement aid, not a step of the method: reads the `bytes` bytes at `buf`
  * (device memory, 16-byte aligned, bytes a multiple of 16) once, with the
  * same non-temporal coalesced 16-byte loads as the row passes.  folds[i]
@@ -397,7 +538,13 @@ typedef enum {
     SV_K_LMHEAD_STATS = 15, /* LM-head projection + row statistics partials and draft logits */
     SV_K_LMHEAD_ROWS = 16,  /* LM-head projection of the rows tokens are drawn from, written */
     SV_K_MERGE_PARTS = 17,  /* row partials merged to one per row (fused projection) */
-    SV_K_COUNT = 18
+    SV_K_APPEND_PAGED = 18, /* norms, rotation and paged cache write of a window */
+    SV_K_ATTEND = 19,       /* attention of a window over a paged cache */
+    SV_K_ATTEND_JOIN = 20,  /* its splits joined */
+    SV_K_COMMIT_PAGED = 21, /* rows of accepted tree paths moved inside a paged cache */
+    SV_K_LOGPROB = 22,      /* row statistics and best tokens per segment */
+    SV_K_LOGPROB_MERGE = 23, /* segments joined: log probabilities, entropy, alternatives */
+    SV_K_COUNT = 24
 } sv_kernel_id;
 
 sv_status sv_trace_begin(int capacity, unsigned kernel_mask);

@@ -1,0 +1,161 @@
+"""Host-side checks of the paged-cache and log-probability entry points (CPU
+only: every call here is refused, or empty, before a device is touched)."""
+
+import ctypes
+
+import pytest
+
+import draft_token_verification_04_amd as sv
+
+FAKE = ctypes.c_void_p(1 << 20)  # non-null, 256-aligned, never dereferenced
+ODD = ctypes.c_void_p((1 << 20) + 8)
+INV, UNS, WS = sv.SV_ERR_INVALID_ARG, sv.SV_ERR_UNSUPPORTED, sv.SV_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sv.load_library()
+
+
+def _cache(**kw):
+    a = dict(k=1 << 20, v=1 << 20, k_scale=None, v_scale=None, dt=sv.SV_BF16, num_pages=8, kv_heads=2, page_size=16,
+             head_dim=128)
+    a.update(kw)
+    return sv._PagedKVStruct(*[a[n] for n, _ in sv._PagedKVStruct._fields_])
+
+
+BAD_CACHES = [(dict(dt=sv.SV_F32), UNS), (dict(dt=7), UNS), (dict(num_pages=0), INV), (dict(kv_heads=0), INV),
+              (dict(page_size=0), INV), (dict(page_size=8), UNS), (dict(page_size=24), UNS),
+              (dict(page_size=2048), UNS), (dict(head_dim=0), INV), (dict(head_dim=96), UNS),
+              (dict(head_dim=512), UNS)]
+BAD_POINTERS = [dict(k=None), dict(v=None), dict(k=(1 << 20) + 8), dict(v=(1 << 20) + 4), dict(dt=sv.SV_E4M3),
+                dict(dt=sv.SV_E4M3, k_scale=1 << 20), dict(dt=sv.SV_E4M3, k_scale=1 << 20, v_scale=(1 << 20) + 4)]
+
+
+def _append(lib, cache=None, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, qs=4 * 128, ks=2 * 128, vs=2 * 128, wq=None, wk=None, eps=1e-6, rope=FAKE, rot=128,
+             max_pos=100, il=0, pos=FAKE, base=FAKE, counts=None, B=2, N=3, H=4, table=FAKE, P=5, out=FAKE, st=None)
+    a.update(kw)
+    return lib.spec_append_kv_paged(a["q"], a["k"], a["v"], a["qs"], a["ks"], a["vs"], a["wq"], a["wk"], a["eps"],
+                                    a["rope"], a["rot"], a["max_pos"], a["il"], a["pos"], a["base"], a["counts"],
+                                    a["B"], a["N"], a["H"], cache or _cache(), a["table"], a["P"], a["out"], a["st"],
+                                    None)
+
+
+def test_append_refusals(lib):
+    for c, want in BAD_CACHES:
+        assert _append(lib, _cache(**c)) == want, c
+    for c in BAD_POINTERS:
+        assert _append(lib, _cache(**c)) == INV, c
+    for kw, want in [(dict(B=-1), INV), (dict(N=0), INV), (dict(H=0), INV), (dict(P=0), INV), (dict(eps=-1.0), INV),
+                     (dict(eps=float("nan")), INV), (dict(eps=float("inf")), INV), (dict(rot=0), INV),
+                     (dict(rot=144), INV), (dict(rot=24), UNS), (dict(max_pos=0), INV), (dict(P=1 << 28), UNS),
+                     (dict(B=1 << 20, N=1 << 20), UNS), (dict(H=1 << 17), UNS), (dict(q=None), INV),
+                     (dict(k=None), INV), (dict(v=None), INV), (dict(base=None), INV), (dict(table=None), INV),
+                     (dict(out=None), INV), (dict(pos=None), INV), (dict(wq=FAKE), INV), (dict(wk=FAKE), INV),
+                     (dict(q=ODD), INV), (dict(k=ODD), INV), (dict(v=ODD), INV), (dict(out=ODD), INV),
+                     (dict(rope=ODD), INV), (dict(wq=ODD, wk=FAKE), INV), (dict(qs=500), INV), (dict(qs=516), INV),
+                     (dict(ks=128), INV), (dict(vs=-256), INV), (dict(qs=1 << 33), UNS)]:
+        assert _append(lib, **kw) == want, kw
+    assert _append(lib, B=0, q=None, out=None) == sv.SV_OK
+
+
+def _attend(lib, cache=None, **kw):
+    a = dict(q=FAKE, qs=4 * 128, table=FAKE, P=5, base=FAKE, counts=None, parents=None, B=2, N=3, H=4, scale=0.1,
+             out=FAKE, lse=None, st=None, ws=FAKE, wsb=0)
+    a.update(kw)
+    return lib.spec_attend_paged(a["q"], a["qs"], cache or _cache(), a["table"], a["P"], a["base"], a["counts"],
+                                 a["parents"], a["B"], a["N"], a["H"], a["scale"], a["out"], a["lse"], a["st"],
+                                 a["ws"], a["wsb"], None)
+
+
+def test_attend_refusals(lib):
+    for c, want in BAD_CACHES:
+        assert _attend(lib, _cache(**c)) == want, c
+    for c in BAD_POINTERS:
+        assert _attend(lib, _cache(**c)) == INV, c
+    for kw, want in [(dict(B=-1), INV), (dict(N=0), INV), (dict(H=0), INV), (dict(H=3), INV), (dict(P=0), INV),
+                     (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV),
+                     (dict(scale=float("inf")), INV), (dict(N=sv.SV_MAX_WINDOW + 1), UNS), (dict(P=1 << 27), UNS),
+                     (dict(B=1 << 30), UNS), (dict(H=1 << 18), UNS), (dict(q=None), INV), (dict(table=None), INV),
+                     (dict(base=None), INV), (dict(out=None), INV), (dict(ws=None), INV), (dict(q=ODD), INV),
+                     (dict(out=ODD), INV), (dict(ws=ODD), INV), (dict(qs=508), INV), (dict(qs=504), INV),
+                     (dict(qs=1 << 33), UNS), (dict(), WS)]:
+        assert _attend(lib, **kw) == want, kw
+    assert _attend(lib, scale=3e38, wsb=1 << 30) == UNS
+    assert _attend(lib, B=0, q=None, ws=None) == sv.SV_OK
+    need = lib.sv_attend_workspace_bytes(2, 3, 4, 2, 128, 5, 16)
+    assert need >= 256 and need % 256 == 0 and _attend(lib, wsb=need - 1) == WS
+
+
+def test_attend_workspace_query(lib):
+    f = lib.sv_attend_workspace_bytes
+    assert f(0, 1, 4, 2, 128, 5, 16) == 0 and f(1, 0, 4, 2, 128, 5, 16) == 0 and f(1, 65, 4, 2, 128, 5, 16) == 0
+    assert f(1, 1, 5, 2, 128, 5, 16) == 0 and f(1, 1, 4, 2, 80, 5, 16) == 0 and f(1, 1, 4, 2, 128, 5, 48) == 0
+    assert f(1, 1, 4, 2, 128, 1 << 27, 16) == 0
+    # one page needs no split; a long table does, and its partials stay far below the cache
+    assert f(1, 1, 32, 8, 128, 1, 16) == 256
+    assert 256 < f(1, 5, 32, 8, 128, 8192, 16) < 8192 * 16 * 8 * 128 * 4
+    assert f(4096, 64, 64, 8, 256, 64, 16) > 0
+
+
+def _commit(lib, **kw):
+    a = dict(pages=FAKE, scales=None, G=2, np=8, h=2, ps=16, rb=256, table=FAKE, P=4, B=3, tb=FAKE, cb=FAKE, d=FAKE,
+             p=FAKE, N=33, st=None)
+    a.update(kw)
+    return lib.spec_commit_tree_kv_paged(a["pages"], a["scales"], a["G"], a["np"], a["h"], a["ps"], a["rb"],
+                                         a["table"], a["P"], a["B"], a["tb"], a["cb"], a["d"], a["p"], a["N"], a["st"],
+                                         None)
+
+
+def test_commit_paged_refusals(lib):
+    for kw, want in [(dict(G=0), INV), (dict(B=-1), INV), (dict(np=0), INV), (dict(h=0), INV), (dict(P=0), INV),
+                     (dict(N=0), INV), (dict(ps=0), INV), (dict(rb=8), INV), (dict(rb=24), INV), (dict(ps=8), UNS),
+                     (dict(ps=40), UNS), (dict(ps=2048), UNS), (dict(rb=48), UNS), (dict(rb=2048), UNS),
+                     (dict(N=sv.SV_MAX_TREE_NODES + 1), UNS), (dict(P=1 << 28), UNS), (dict(G=1 << 20, B=1 << 12), UNS),
+                     (dict(pages=None), INV), (dict(table=None), INV), (dict(tb=None), INV), (dict(cb=None), INV),
+                     (dict(d=None), INV), (dict(p=None), INV), (dict(pages=ODD), INV)]:
+        assert _commit(lib, **kw) == want, kw
+    assert _commit(lib, B=0, pages=None) == sv.SV_OK
+
+
+def _logprobs(lib, **kw):
+    a = dict(x=FAKE, t=FAKE, R=4, V=100, dt=sv.SV_BF16, T=1.0, k=5, lp=FAKE, e=FAKE, ids=FAKE, tl=FAKE, st=None, ws=FAKE,
+             wsb=0)
+    a.update(kw)
+    return lib.spec_token_logprobs(a["x"], a["t"], a["R"], a["V"], a["dt"], a["T"], a["k"], a["lp"], a["e"], a["ids"],
+                                   a["tl"], a["st"], a["ws"], a["wsb"], None)
+
+
+def test_token_logprobs_refusals(lib):
+    for kw, want in [(dict(dt=sv.SV_E4M3), UNS), (dict(dt=9), UNS), (dict(R=-1), INV), (dict(V=0), INV), (dict(k=-1), INV),
+                     (dict(V=4), INV), (dict(k=sv.SV_MAX_TOP + 1), UNS), (dict(T=0.0), INV), (dict(T=-2.0), INV),
+                     (dict(T=float("nan")), INV), (dict(T=float("inf")), INV), (dict(V=1 << 30), UNS),
+                     (dict(x=None), INV), (dict(t=None), INV), (dict(ids=None), INV), (dict(tl=None), INV),
+                     (dict(ws=None), INV), (dict(ws=ODD), INV), (dict(x=ctypes.c_void_p((1 << 20) + 1)), INV),
+                     (dict(dt=sv.SV_F32, x=ctypes.c_void_p((1 << 20) + 2)), INV), (dict(), WS)]:
+        assert _logprobs(lib, **kw) == want, kw
+    need = lib.sv_token_logprobs_workspace_bytes(4, 100, sv.SV_BF16, 5)
+    assert need > 0 and _logprobs(lib, wsb=need - 1) == WS
+    assert _logprobs(lib, wsb=need, T=1e-40) == UNS
+    assert _logprobs(lib, R=0, x=None, ws=None) == sv.SV_OK
+    f = lib.sv_token_logprobs_workspace_bytes
+    assert f(0, 100, 1, 0) == 0 and f(1, 0, 1, 0) == 0 and f(1, 100, 2, 0) == 0 and f(1, 100, 1, 33) == 0
+    assert f(1, 4, 1, 5) == 0 and f(1, 100, 1, -1) == 0
+
+
+def test_existing_entry_points_refuse_the_cache_dtype(lib):
+    assert lib.sv_sample_workspace_bytes(2, 3, 100, sv.SV_E4M3) == 0
+    assert lib.sv_greedy_workspace_bytes(2, 3, 100, sv.SV_E4M3) == 0
+
+
+def test_constants_match_the_header():
+    import os
+    import re
+
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                             "spec_verify.h")).read()
+    consts = {m.group(1): int(m.group(2)) for m in re.finditer(r"\b(SV_[A-Z0-9_]+)\s*=\s*(\d+)", text)}
+    consts.update({m.group(1): int(m.group(2)) for m in re.finditer(r"#define\s+(SV_[A-Z_]+)\s+(\d+)", text)})
+    for name in ("SV_E4M3", "SV_MAX_WINDOW", "SV_MAX_TOP"):
+        assert getattr(sv, name) == consts[name], name
