@@ -156,12 +156,18 @@ def version() -> str:
 
 # ---- helpers -------------------------------------------------------------------
 
-def _torch():
-    import torch
+_torch_module = None
 
-    if not torch.cuda.is_available():
-        raise RuntimeError("specverify needs a ROCm GPU; none is visible")
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        if not torch.cuda.is_available():
+            raise RuntimeError("specverify needs a ROCm GPU; none is visible")
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -197,6 +203,18 @@ def _ptr(t):
 def _stream(torch, device, stream):
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _call(torch, fn, device, stream, *args):
+    """fn(*args, stream) with `device` current.  A call on the current device's
+    current stream, the usual one, takes neither a device guard nor a stream
+    object (4 us of a call's 16)."""
+    if device.index == torch.cuda.current_device():
+        if stream is None:
+            return fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+        return fn(*args, stream.cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, _stream(torch, device, stream))
 
 
 def _hold(torch, device, stream, *tensors):
@@ -698,12 +716,11 @@ def spec_append_kv_paged(q, k, v, cache, page_table, base, positions=None, *, q_
     out = dict(q=_window_out(torch, q_out, "q_out", (B, N, H, D), torch.bfloat16, dev))
     if status:
         out["status"] = torch.empty((B, N), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        rc = lib.spec_append_kv_paged(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_weight), _ptr(k_weight), float(eps),
-            _ptr(rope), rot, max_pos, int(bool(interleaved)), _ptr(positions), base.data_ptr(), _ptr(counts),
-            B, N, H, cache._c, page_table.data_ptr(), page_table.shape[1], out["q"].data_ptr(),
-            _ptr(out.get("status")), _stream(torch, dev, stream))
+    rc = _call(
+        torch, lib.spec_append_kv_paged, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope), rot, max_pos, int(bool(interleaved)), _ptr(positions), base.data_ptr(), _ptr(counts),
+        B, N, H, cache._c, page_table.data_ptr(), page_table.shape[1], out["q"].data_ptr(),
+        _ptr(out.get("status")))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_append_kv_paged")
     _hold(torch, dev, stream, *out.values())
@@ -745,11 +762,10 @@ def spec_attend_paged(q, cache, page_table, base, *, parents=None, counts=None, 
         res["status"] = torch.empty(B, dtype=torch.int32, device=dev)
     ws = _workspace(torch, lib.sv_attend_workspace_bytes(B, N, H, cache.kv_heads, D, P, cache.page_size), dev,
                     workspace)
-    with torch.cuda.device(dev):
-        rc = lib.spec_attend_paged(
-            q.data_ptr(), qs, cache._c, page_table.data_ptr(), P, base.data_ptr(), _ptr(counts), _ptr(parents),
-            B, N, H, float(D ** -0.5 if scale is None else scale), res["out"].data_ptr(), _ptr(res.get("lse")),
-            _ptr(res.get("status")), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(torch, dev, stream))
+    rc = _call(
+        torch, lib.spec_attend_paged, dev, stream, q.data_ptr(), qs, cache._c, page_table.data_ptr(), P,
+        base.data_ptr(), _ptr(counts), _ptr(parents), B, N, H, float(D ** -0.5 if scale is None else scale), res["out"].data_ptr(), _ptr(res.get("lse")),
+        _ptr(res.get("status")), ws.data_ptr(), ws.numel() * ws.element_size())
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_attend_paged")
     _hold(torch, dev, stream, ws if workspace is None else None, *res.values())
@@ -782,11 +798,10 @@ def spec_commit_tree_kv_paged(pages, page_table, tree_base, commit_base, accept_
     if path.shape[0] != B:
         raise ValueError("path must be [B, N]")
     st = torch.empty(B, dtype=torch.int32, device=dev) if status else None
-    with torch.cuda.device(dev):
-        rc = lib.spec_commit_tree_kv_paged(
-            pages.data_ptr(), _ptr(scales), G, num_pages, kv_heads, page_size, D * pages.element_size(),
-            page_table.data_ptr(), P, B, tree_base.data_ptr(), commit_base.data_ptr(), accept_len.data_ptr(),
-            path.data_ptr(), path.shape[1], _ptr(st), _stream(torch, dev, stream))
+    rc = _call(
+        torch, lib.spec_commit_tree_kv_paged, dev, stream, pages.data_ptr(), _ptr(scales), G, num_pages, kv_heads,
+        page_size, D * pages.element_size(), page_table.data_ptr(), P, B, tree_base.data_ptr(), commit_base.data_ptr(), accept_len.data_ptr(),
+        path.data_ptr(), path.shape[1], _ptr(st))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_commit_tree_kv_paged")
     _hold(torch, dev, stream, st)
@@ -822,11 +837,10 @@ def spec_token_logprobs(logits, tokens=None, *, temperature=1.0, top_k=0, entrop
     if status:
         out["status"] = torch.empty(R, dtype=torch.int32, device=dev)
     ws = _workspace(torch, lib.sv_token_logprobs_workspace_bytes(R, V, dt, top_k), dev, workspace)
-    with torch.cuda.device(dev):
-        rc = lib.spec_token_logprobs(
-            logits.data_ptr(), _ptr(tokens), R, V, dt, float(temperature), top_k, _ptr(out.get("logprob")),
-            _ptr(out.get("entropy")), _ptr(out.get("top_ids")), _ptr(out.get("top_logprobs")),
-            _ptr(out.get("status")), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(torch, dev, stream))
+    rc = _call(
+        torch, lib.spec_token_logprobs, dev, stream, logits.data_ptr(), _ptr(tokens), R, V, dt, float(temperature),
+        top_k, _ptr(out.get("logprob")), _ptr(out.get("entropy")), _ptr(out.get("top_ids")), _ptr(out.get("top_logprobs")),
+        _ptr(out.get("status")), ws.data_ptr(), ws.numel() * ws.element_size())
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_token_logprobs")
     _hold(torch, dev, stream, ws if workspace is None else None, *out.values())

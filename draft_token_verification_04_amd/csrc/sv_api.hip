@@ -862,13 +862,13 @@ sv_status spec_commit_tree_kv_paged(void *pages, float *scales, int G, int num_p
 
 namespace {
 struct LogprobWs {
-    size_t keys, total;
+    size_t group_maxima, total;
 };
 LogprobWs logprob_ws_layout(int R, int V, sv_dtype dt, int k) {
     const size_t n = static_cast<size_t>(R) * static_cast<size_t>(logprob_segs(R, V, dt));
     LogprobWs w;
-    w.keys = align_up(n * sizeof(LogprobPart));
-    w.total = w.keys + align_up(n * static_cast<size_t>(k) * sizeof(uint64_t));
+    w.group_maxima = align_up(n * sizeof(LogprobPart));
+    w.total = w.group_maxima + (k > 0 ? align_up(n * 64 * sizeof(float)) : 0);
     return w;
 }
 }  // namespace
@@ -900,7 +900,7 @@ sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, 
     if (workspace_bytes < L.total) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
     const LogprobArgs a = {logits, tokens, R, V, segs, top_k, static_cast<float>(c),
-                           reinterpret_cast<LogprobPart *>(ws), reinterpret_cast<uint64_t *>(ws + L.keys),
+                           reinterpret_cast<LogprobPart *>(ws), reinterpret_cast<float *>(ws + L.group_maxima),
                            logprob, entropy, top_ids, top_logprobs, row_status};
     hipError_t e = traced(SV_K_LOGPROB, stream, [&] { return launch_logprob(a, dt, stream); });
     if (e == hipSuccess)

@@ -269,7 +269,7 @@ struct LogprobArgs {
     int R, V, segs, k;
     float c;
     LogprobPart *parts;  // [R][segs]
-    uint64_t *keys;      // [R][segs][k]
+    float *group_maxima;     // [R][segs][64] (k > 0)
     float *logprob, *entropy;
     int32_t *top_ids;
     float *top_logprobs;
