@@ -841,7 +841,7 @@ sv_status spec_commit_tree_kv_paged(void *pages, float *scales, int G, int num_p
         row_bytes % 16 != 0)
         return SV_ERR_INVALID_ARG;
     if (!power_of_two(page_size) || page_size < 16 || page_size > 1024 || !power_of_two(row_bytes) ||
-        row_bytes > 1024 || N > SV_MAX_TREE_NODES || static_cast<long long>(P) * page_size > 0x7fffffffLL ||
+        row_bytes > 1024 || N > SV_MAX_TREE_NODES || kv_heads > 32768 || static_cast<long long>(P) * page_size > 0x7fffffffLL ||
         static_cast<double>(G) * B * kv_heads > 2.0e9)
         return SV_ERR_UNSUPPORTED;
     if (static_cast<double>(G) * num_pages * kv_heads * page_size * row_bytes >= 9.0e18) return SV_ERR_UNSUPPORTED;
