@@ -152,14 +152,14 @@ __global__ __launch_bounds__(kBlock) void k_append(AppendArgs a) {
                     ((static_cast<long long>(page) * a.Hkv + head) << a.page_shift) + in_page;
                 dst = static_cast<uint16_t *>(kind == 1 ? a.k_pages : a.v_pages) + row * D;
             }
-            *reinterpret_cast<uint4 *>(dst + d0) = o;
+            __builtin_nontemporal_store(u32x4{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4 *>(dst + d0));
         } else {
             const long long row = ((static_cast<long long>(page) * a.Hkv + head) << a.page_shift) + in_page;
             uint8_t *dst = static_cast<uint8_t *>(kind == 1 ? a.k_pages : a.v_pages) + row * D;
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] *= inv;
-            *reinterpret_cast<uint2 *>(dst + d0) =
-                make_uint2(pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7]));
+            __builtin_nontemporal_store(u32x2{pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7])},
+                                        reinterpret_cast<u32x2 *>(dst + d0));
             if (c == 0) (kind == 1 ? a.k_scale : a.v_scale)[row] = fmaxf(top, top > 0.0f ? kMinAmax : 0.0f) / 448.0f;
         }
     }
