@@ -173,10 +173,15 @@ hipError_t launch_d(const AppendArgs &a, bool e4m3, dim3 grid, hipStream_t s) {
 
 }  // namespace
 
+// Tokens from which a workgroup takes all of a token's rows, in passes, instead
+// of one pass's: lookups and angles are then read once per token.  8191 tokens of
+// 48 rows: 46 us against 61; 2112 (most of them padding): 11.4 against 10.8.
+constexpr int kWideTokens = 4096;
+
 hipError_t launch_append(const AppendArgs &a, int D, bool e4m3, int tokens, hipStream_t s) {
     const int rows = a.H + 2 * a.Hkv, per = kBlock / (D / 8);
     const int passes = (rows + per - 1) / per;
-    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(passes));
+    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(tokens >= kWideTokens ? 1 : passes));
     if (D == 64) return launch_d<64>(a, e4m3, grid, s);
     if (D == 128) return launch_d<128>(a, e4m3, grid, s);
     return launch_d<256>(a, e4m3, grid, s);
