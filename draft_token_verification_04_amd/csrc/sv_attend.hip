@@ -45,6 +45,7 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 32;  // slots a wave takes per step
+constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ f32x4 mfma16(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -119,22 +120,112 @@ __device__ __forceinline__ bf16x8 widen8(unsigned lo, unsigned hi) {
     return as_bf16x8(e4m3_to_bf16<false>(lo), e4m3_to_bf16<true>(lo), e4m3_to_bf16<false>(hi), e4m3_to_bf16<true>(hi));
 }
 
+// Whether a word of cached values holds an infinity or NaN, and the word with
+// those cleared.
+template <bool E4M3>
 __device__ __forceinline__ bool has_nonfinite(unsigned w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    if constexpr (E4M3) {  // a byte of 0x7f or 0xff: the low 7 bits + 1 carry into bit 7
+        return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    } else {
+        return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    }
 }
-// The word with its non-finite halves cleared.
+template <bool E4M3>
 __device__ __forceinline__ unsigned finite_only(unsigned w) {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-    return w;
+    if constexpr (E4M3) {
+        const unsigned m = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+        return w & ~(m * 0xffu);
+    } else {
+        if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+        if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+        return w;
+    }
 }
 
+// The cached rows of one tile as they lie in memory: the lane's slices of K (row
+// lane % 16 of each half, for the left operand) and its 8 rows of V.
+template <int D, bool E4M3>
+struct Tile {
+    static constexpr int kElem = E4M3 ? 1 : 2;
+    static constexpr int kKVecs = D * kElem / 64;      // 16-byte loads of a K row per lane
+    static constexpr int kVWords = D * kElem / 64;     // words of a V row per lane (D / 16 values)
+    static constexpr int kWordVals = 4 / kElem;        // values per word
+    u32x4 k[2][kKVecs];
+    unsigned v[2][4][kVWords];
+    f32x4 ks[2], vs[2];  // e4m3: the rows' scales, in the order of the scores
+
+    __device__ __forceinline__ void load_k(const AttendArgs &a, const long long (&row)[2], int col, int kg) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const char *p = static_cast<const char *>(a.k_pages) + (row[f] + col) * (D * kElem) + kg * 16;
+#pragma unroll
+            for (int c = 0; c < kKVecs; ++c) k[f][c] = *reinterpret_cast<const u32x4 *>(p + c * 64);
+            if constexpr (E4M3) ks[f] = *reinterpret_cast<const f32x4 *>(a.k_scale + row[f] + kg * 4);
+        }
+    }
+    __device__ __forceinline__ void load_v(const AttendArgs &a, const long long (&row)[2], int col, int kg) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned *p = reinterpret_cast<const unsigned *>(
+                    static_cast<const char *>(a.v_pages) + (row[f] + kg * 4 + j) * (D * kElem) + col * (kVWords * 4));
+#pragma unroll
+                for (int i = 0; i < kVWords; ++i) v[f][j][i] = p[i];
+            }
+            if constexpr (E4M3) vs[f] = *reinterpret_cast<const f32x4 *>(a.v_scale + row[f] + kg * 4);
+        }
+    }
+    // The left operand of the 32 values of step c of the first product.
+    __device__ __forceinline__ bf16x8 k_slice(int f, int c) const {
+        if constexpr (E4M3)
+            return c % 2 ? widen8(k[f][c / 2].z, k[f][c / 2].w) : widen8(k[f][c / 2].x, k[f][c / 2].y);
+        else
+            return __builtin_bit_cast(bf16x8, k[f][c]);
+    }
+    // V^T of word i: for each of its values the lane's 8 slots, in the order (half, slot).
+    __device__ __forceinline__ void transpose(int i, bf16x8 (&vt)[kWordVals]) const {
+        unsigned x[kWordVals][4];  // [value][pair of slots]
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const unsigned even = v[f][2 * j][i], odd = v[f][2 * j + 1][i];
+                if constexpr (E4M3) {
+                    // bytes of two slots side by side, then widened in pairs
+                    const unsigned lo = __builtin_amdgcn_perm(odd, even, 0x05010400u);
+                    const unsigned hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+                    x[0][2 * f + j] = e4m3_to_bf16<false>(lo);
+                    x[1][2 * f + j] = e4m3_to_bf16<true>(lo);
+                    x[2][2 * f + j] = e4m3_to_bf16<false>(hi);
+                    x[3][2 * f + j] = e4m3_to_bf16<true>(hi);
+                } else {
+                    x[0][2 * f + j] = __builtin_amdgcn_perm(odd, even, 0x05040100u);
+                    x[1][2 * f + j] = __builtin_amdgcn_perm(odd, even, 0x07060302u);
+                }
+            }
+#pragma unroll
+        for (int e = 0; e < kWordVals; ++e) vt[e] = as_bf16x8(x[e][0], x[e][1], x[e][2], x[e][3]);
+    }
+};
+
 template <int D, bool E4M3, int QT>
-__global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     constexpr int kChunks = D / 32;       // 32-value steps of the first product
     constexpr int kVals = D / 16;         // values per lane of V: one MFMA each
-    constexpr int kWords = kVals / 2;     // packed pairs
-    constexpr int kElem = E4M3 ? 1 : 2;
+    constexpr bool kQInLds = QT > 1 || D == 256;
+    // where the registers just suffice, loads and widenings stay where they are
+    // written: moved ahead, as the compiler likes to, they spill (64 requests of 33
+    // rows, QT = 3: 203 us, and 120 us in place)
+    constexpr bool kTight = QT * D > 256 || D == 256;
+    constexpr int kPad = 4;
+    // the queries during the walk, the four waves' rows at the end
+    __shared__ union {
+        u32x4 q[kQInLds ? QT : 1][kChunks][kWave];
+        float o[kWavesPerBlock][16][D + kPad];
+    } lds;
+    __shared__ float sm[kWavesPerBlock][16], sl[kWavesPerBlock][16];
+    __shared__ int sbad;
     const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
     const int col = lane & 15, kg = lane >> 4;
 
@@ -166,9 +257,11 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
     }
     if (split >= sp.active) return;
 
-    // this lane's query rows: the right operand's column `col` of each row tile
-    bf16x8 qf[QT][kChunks];
+    // this lane's query rows: the right operand's column `col` of each row tile.
+    // One row tile's slices stay in registers; more of them are shared by the
+    // workgroup's waves through LDS, [row tile][step][lane]
     uint64_t sees[QT];
+    u32x4 qr[kQInLds ? 1 : QT][kChunks];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int r = row0 + t * 16 + col;
@@ -178,13 +271,24 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
         const uint16_t *q = a.q + (static_cast<long long>(b) * a.N + n) * a.q_stride + static_cast<long long>(h * a.G + g) * D;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            // e4m3 rows are read 16 values per lane, which are two chunks' slices
+            if (kQInLds && (t * kChunks + c) % kWavesPerBlock != w) continue;
+            // e4m3 rows are read 16 values per lane, which are two steps' slices
             const int d = E4M3 ? (c / 2) * 64 + kg * 16 + (c % 2) * 8 : c * 32 + kg * 8;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = *reinterpret_cast<const uint4 *>(q + d);
-            qf[t][c] = as_bf16x8(x.x, x.y, x.z, x.w);
+            u32x4 x = {0, 0, 0, 0};
+            if (live) x = *reinterpret_cast<const u32x4 *>(q + d);
+            if constexpr (kQInLds)
+                lds.q[t][c][lane] = x;
+            else
+                qr[t][c] = x;
         }
     }
+    if constexpr (kQInLds) __syncthreads();
+    auto q_slice = [&](int t, int c) {
+        if constexpr (kQInLds)
+            return __builtin_bit_cast(bf16x8, lds.q[t][c][lane]);
+        else
+            return __builtin_bit_cast(bf16x8, qr[t][c]);
+    };
 
     f32x4 o[QT][kVals];
     float m[QT], l[QT];
@@ -198,80 +302,71 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
 
     const int32_t *table = a.page_table + static_cast<long long>(b) * a.P;
     const int page_mask = (1 << a.page_shift) - 1;
-    const char *kp = static_cast<const char *>(a.k_pages), *vp = static_cast<const char *>(a.v_pages);
     bool bad = false;
     const int t0 = (split * kWavesPerBlock + w) * sp.per_wave;
     const int t1 = min(t0 + sp.per_wave, sp.tiles);
-    for (int tile = t0; tile < t1; ++tile) {
-        const int s0 = tile * kTile;
-        // row (in units of rows) of the first slot of each 16-slot half
-        long long row[2];
+    int ids = 0;  // lane i: the page of the i-th 16 slots of 32 tiles
+    // rows (in units of rows) of the first slots of a tile's two 16-slot halves;
+    // tiles are asked for in order
+    auto find_rows = [&](int tile, long long (&row)[2]) {
+        const int half0 = ((tile - t0) & 31) * 2;
+        if (half0 == 0) {
+            const int s = tile * kTile + 16 * lane;
+            ids = s < sp.total ? table[s >> a.page_shift] : 0;
+            const bool out = ids < 0 || ids >= a.num_pages;
+            bad |= out && s < t1 * kTile;
+            if (out) ids = 0;
+        }
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            const int s = s0 + 16 * f < sp.total ? s0 + 16 * f : s0;
-            int page = uniform(table[s >> a.page_shift]);
-            if (page < 0 || page >= a.num_pages) {
-                bad = true;
-                page = 0;
-            }
+            // a half behind the last slot reads the first half's rows
+            const bool there = tile * kTile + 16 * f < sp.total;
+            const int s = tile * kTile + (there ? 16 * f : 0);
+            const int page = __builtin_amdgcn_readlane(ids, half0 + (there ? f : 0));
             row[f] = ((static_cast<long long>(page) * a.Hkv + h) << a.page_shift) + (s & page_mask);
         }
-        bf16x8 kf[2][kChunks];
-        unsigned vw[2][4][kWords];  // [half][slot][pair of values]
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            const char *p = kp + (row[f] + col) * (D * kElem);
-            if constexpr (E4M3) {
-#pragma unroll
-                for (int c = 0; c < kChunks; c += 2) {
-                    const u32x4 x = *reinterpret_cast<const u32x4 *>(p + c * 32 + kg * 16);
-                    kf[f][c] = widen8(x.x, x.y);
-                    kf[f][c + 1] = widen8(x.z, x.w);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    kf[f][c] = *reinterpret_cast<const bf16x8 *>(p + (c * 32 + kg * 8) * 2);
-            }
-        }
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const char *p = vp + (row[f] + kg * 4 + j) * (D * kElem) + col * (kVals * kElem);
-                if constexpr (E4M3) {
-#pragma unroll
-                    for (int i = 0; i < kVals / 4; ++i) {
-                        const unsigned x = reinterpret_cast<const unsigned *>(p)[i];
-                        vw[f][j][2 * i] = e4m3_to_bf16<false>(x);
-                        vw[f][j][2 * i + 1] = e4m3_to_bf16<true>(x);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kWords; ++i) vw[f][j][i] = reinterpret_cast<const unsigned *>(p)[i];
-                }
-            }
-        f32x4 ks[2], vs[2];
-        if constexpr (E4M3) {
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                ks[f] = *reinterpret_cast<const f32x4 *>(a.k_scale + row[f] + kg * 4);
-                vs[f] = *reinterpret_cast<const f32x4 *>(a.v_scale + row[f] + kg * 4);
-            }
-        }
+    };
+    // a tile's K is replaced by the next tile's as soon as the scores are formed,
+    // its V once it is transposed, so a wave always has loads in flight
+    Tile<D, E4M3> kv;
+    long long row[2], next[2];
+    if (t0 < t1) {
+        find_rows(t0, next);
+        kv.load_k(a, next, col, kg);
+        kv.load_v(a, next, col, kg);
+    }
+    for (int tile = t0; tile < t1; ++tile) {
+        const int s0 = tile * kTile;
+        const bool more = tile + 1 < t1;
+        row[0] = next[0];
+        row[1] = next[1];
+        if (more) find_rows(tile + 1, next);
 
         // scores: slot s0 + 16 f + 4 kg + j of row col
         f32x4 sc[QT][2];
 #pragma unroll
-        for (int t = 0; t < QT; ++t)
+        for (int t = 0; t < QT; ++t) sc[t][0] = sc[t][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                f32x4 x = {0, 0, 0, 0};
+        for (int c = 0; c < kChunks; ++c) {
+            if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);  // no slice read long before its use
+            const bf16x8 k0 = kv.k_slice(0, c), k1 = kv.k_slice(1, c);
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) x = mfma16(kf[f][c], qf[t][c], x);
-                if constexpr (E4M3) x *= ks[f];
-                sc[t][f] = x;
+            for (int t = 0; t < QT; ++t) {
+                const bf16x8 q = q_slice(t, c);
+                sc[t][0] = mfma16(k0, q, sc[t][0]);
+                sc[t][1] = mfma16(k1, q, sc[t][1]);
             }
+        }
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                sc[t][0] *= kv.ks[0];
+                sc[t][1] *= kv.ks[1];
+            }
+        }
+        if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
+        if (more) kv.load_k(a, next, col, kg);
+        if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
         const bool edge = s0 + kTile > sp.base;  // slots of the window, or behind it
         bool odd = false;                        // a window token has a non-finite value
         if (edge) {
@@ -282,10 +377,10 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
                     const int s = s0 + 16 * f + 4 * kg + j;
                     if (s >= sp.base) {
 #pragma unroll
-                        for (int i = 0; i < kWords; ++i) {
-                            if (s >= sp.total) vw[f][j][i] = 0;
-                            odd |= has_nonfinite(vw[f][j][i]);
-                            vw[f][j][i] = finite_only(vw[f][j][i]);
+                        for (int i = 0; i < kv.kVWords; ++i) {
+                            if (s >= sp.total) kv.v[f][j][i] = 0;
+                            odd |= has_nonfinite<E4M3>(kv.v[f][j][i]);
+                            kv.v[f][j][i] = finite_only<E4M3>(kv.v[f][j][i]);
                         }
                     }
 #pragma unroll
@@ -296,28 +391,16 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
             odd = ballot(odd) != 0;
         }
 
-        // V^T: for each of the lane's values its 8 slots, in the order (half, slot)
-        bf16x8 vt[kVals];
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            unsigned lo[4], hi[4];
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    lo[2 * f + j] = __builtin_amdgcn_perm(vw[f][2 * j + 1][i], vw[f][2 * j][i], 0x05040100u);
-                    hi[2 * f + j] = __builtin_amdgcn_perm(vw[f][2 * j + 1][i], vw[f][2 * j][i], 0x07060302u);
-                }
-            vt[2 * i] = as_bf16x8(lo[0], lo[1], lo[2], lo[3]);
-            vt[2 * i + 1] = as_bf16x8(hi[0], hi[1], hi[2], hi[3]);
-        }
-
+        bf16x8 pf[QT];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
+            if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
             float top = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3]));
             top = fmaxf(top, fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-            top = fmaxf(m[t], quad_max(top));
-            if (ballot(top > m[t]) != 0) {
+            // the reference stays while no weight exceeds 2^kSlack: one exponent more
+            // or less costs fp32 sums and bf16 weights nothing
+            if (ballot((top - m[t]) * a.c > kSlack || m[t] == -__builtin_huge_valf()) != 0) {
+                top = fmaxf(m[t], quad_max(top));
                 const float f = m[t] == -__builtin_huge_valf() ? 0.0f : fast_exp2((m[t] - top) * a.c);
                 l[t] *= f;
 #pragma unroll
@@ -327,32 +410,42 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
             const float ref = m[t] == -__builtin_huge_valf() ? 0.0f : m[t] * a.c;
             float p[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[e] = fast_exp2(fmaf(sc[t][e / 4][e % 4], a.c, -ref));
-                l[t] += p[e];
-            }
+            for (int e = 0; e < 8; ++e) p[e] = fast_exp2(fmaf(sc[t][e / 4][e % 4], a.c, -ref));
+            l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
             if constexpr (E4M3) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float x = p[e] * vs[e / 4][e % 4];
+                    const float x = p[e] * kv.vs[e / 4][e % 4];
                     p[e] = edge && sc[t][e / 4][e % 4] == -__builtin_huge_valf() ? 0.0f : x;
                 }
             }
-            const bf16x8 pf = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
-                                        pack_bf16(p[6], p[7]));
+            pf[t] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+        }
 #pragma unroll
-            for (int i = 0; i < kVals; ++i) o[t][i] = mfma16(vt[i], pf, o[t][i]);
-            if (odd) {
-                // the non-finite values, one by one, for the rows that see their token
-                for (int s = max(s0, sp.base); s < min(s0 + kTile, sp.total); ++s) {
-                    const int e = s - s0;
+        for (int i = 0; i < kv.kVWords; ++i) {
+            if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
+            bf16x8 vt[kv.kWordVals];
+            kv.transpose(i, vt);
+#pragma unroll
+            for (int e = 0; e < kv.kWordVals; ++e)
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+                    o[t][i * kv.kWordVals + e] = mfma16(vt[e], pf[t], o[t][i * kv.kWordVals + e]);
+        }
+        if (more) kv.load_v(a, next, col, kg);
+        if (odd) {
+            // the non-finite values, one by one, for the rows that see their token
+            for (int s = max(s0, sp.base); s < min(s0 + kTile, sp.total); ++s) {
+                const int e = s - s0;
+                const long long at = (row[e / 16] + e % 16) * D;
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
                     float mine = 0.0f;
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
-                        if (x == (e / 16) * 4 + e % 4) mine = p[x];
+                        if (x == (e / 16) * 4 + e % 4) mine = static_cast<float>(pf[t][x]);
                     const float weight = __shfl(mine, (e % 16) / 4 * 16 + col, kWave);
                     if (!((sees[t] >> (s - sp.base)) & 1)) continue;
-                    const long long at = (row[e / 16] + e % 16) * D;
 #pragma unroll
                     for (int i = 0; i < kVals; ++i)
 #pragma unroll
@@ -360,9 +453,9 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
                             const int d = (kg * 4 + j) * kVals + i;
                             float v;
                             if constexpr (E4M3)
-                                v = __uint_as_float(e4m3_to_bf16<false>(reinterpret_cast<const uint8_t *>(vp)[at + d]) << 16);
+                                v = __uint_as_float(e4m3_to_bf16<false>(static_cast<const uint8_t *>(a.v_pages)[at + d]) << 16);
                             else
-                                v = bf16_to_f32(reinterpret_cast<const uint16_t *>(vp)[at + d]);
+                                v = bf16_to_f32(static_cast<const uint16_t *>(a.v_pages)[at + d]);
                             if (!isfinite(v)) o[t][i][j] += weight * v;
                         }
                 }
@@ -371,10 +464,6 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
     }
 
     // join the four waves' rows through LDS, one row tile at a time
-    constexpr int kPad = 4;
-    __shared__ float so[kWavesPerBlock][16][D + kPad];
-    __shared__ float sm[kWavesPerBlock][16], sl[kWavesPerBlock][16];
-    __shared__ int sbad;
     if (threadIdx.x == 0) sbad = 0;
     __syncthreads();
     if (bad) sbad = 1;
@@ -392,7 +481,7 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < kVals; i += 4)
-                *reinterpret_cast<float4 *>(&so[w][col][(kg * 4 + j) * kVals + i]) =
+                *reinterpret_cast<float4 *>(&lds.o[w][col][(kg * 4 + j) * kVals + i]) =
                     make_float4(o[t][i][j], o[t][i + 1][j], o[t][i + 2][j], o[t][i + 3][j]);
         __syncthreads();
         for (int i = threadIdx.x; i < 16 * (D / 4); i += kBlock) {
@@ -407,7 +496,7 @@ __global__ __launch_bounds__(kBlock) void k_attend(AttendArgs a) {
                 if (sm[v][rr] == -__builtin_huge_valf()) continue;
                 const float f = fast_exp2((sm[v][rr] - M) * a.c);
                 L += sl[v][rr] * f;
-                const float4 y = *reinterpret_cast<const float4 *>(&so[v][rr][d]);
+                const float4 y = *reinterpret_cast<const float4 *>(&lds.o[v][rr][d]);
                 x.x += y.x * f;
                 x.y += y.y * f;
                 x.z += y.z * f;
@@ -488,12 +577,13 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_r
 
 template <int D, bool E4M3>
 hipError_t launch_qt(const AttendArgs &a, int QT, dim3 grid, hipStream_t s) {
-    if (QT == 1) return launch_kernel(k_attend<D, E4M3, 1>, grid, dim3(kBlock), 0, s, a);
     if constexpr (D <= 128) {
+        if (QT == 2) return launch_kernel(k_attend<D, E4M3, 2>, grid, dim3(kBlock), 0, s, a);
         if (QT == 3) return launch_kernel(k_attend<D, E4M3, 3>, grid, dim3(kBlock), 0, s, a);
-        if (QT == 4) return launch_kernel(k_attend<D, E4M3, 4>, grid, dim3(kBlock), 0, s, a);
     }
-    return launch_kernel(k_attend<D, E4M3, 2>, grid, dim3(kBlock), 0, s, a);
+    if constexpr (D == 64)
+        if (QT == 4) return launch_kernel(k_attend<D, E4M3, 4>, grid, dim3(kBlock), 0, s, a);
+    return launch_kernel(k_attend<D, E4M3, 1>, grid, dim3(kBlock), 0, s, a);
 }
 
 }  // namespace
@@ -502,7 +592,7 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     constexpr int kTargetGroups = 1024;  // workgroups a call aims for
     AttendPlan p;
     const int rows = N * (H / Hkv), tiles = (rows + 15) / 16;
-    const int most = D <= 128 ? 4 : 2;  // row tiles whose accumulators a wave holds
+    const int most = D == 64 ? 4 : (D == 128 ? 3 : 1);  // row tiles whose accumulators a wave can hold
     p.QB = (tiles + most - 1) / most;
     p.QT = (tiles + p.QB - 1) / p.QB;
     p.min_tiles = p.QT == 1 ? 2 : 4;
