@@ -142,13 +142,23 @@ __device__ __forceinline__ unsigned finite_only(unsigned w) {
     }
 }
 
+// 16, 8 or 4 bytes of the cache; STREAM: past the caches.
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load_cached(const void *p) {
+    if constexpr (STREAM)
+        return __builtin_nontemporal_load(static_cast<const T *>(p));
+    else
+        return *static_cast<const T *>(p);
+}
+
 // The cached rows of one tile as they lie in memory: the lane's slices of K (row
 // lane % 16 of each half, for the left operand) and its 8 rows of V.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool STREAM>
 struct Tile {
     static constexpr int kElem = E4M3 ? 1 : 2;
     static constexpr int kKVecs = D * kElem / 64;      // 16-byte loads of a K row per lane
     static constexpr int kVWords = D * kElem / 64;     // words of a V row per lane (D / 16 values)
+    static constexpr int kVStep = kVWords < 4 ? kVWords : 4;
     static constexpr int kWordVals = 4 / kElem;        // values per word
     u32x4 k[2][kKVecs];
     unsigned v[2][4][kVWords];
@@ -159,7 +169,7 @@ struct Tile {
         for (int f = 0; f < 2; ++f) {
             const char *p = static_cast<const char *>(a.k_pages) + (row[f] + col) * (D * kElem) + kg * 16;
 #pragma unroll
-            for (int c = 0; c < kKVecs; ++c) k[f][c] = *reinterpret_cast<const u32x4 *>(p + c * 64);
+            for (int c = 0; c < kKVecs; ++c) k[f][c] = load_cached<STREAM, u32x4>(p + c * 64);
             if constexpr (E4M3) ks[f] = *reinterpret_cast<const f32x4 *>(a.k_scale + row[f] + kg * 4);
         }
     }
@@ -171,7 +181,19 @@ struct Tile {
                 const unsigned *p = reinterpret_cast<const unsigned *>(
                     static_cast<const char *>(a.v_pages) + (row[f] + kg * 4 + j) * (D * kElem) + col * (kVWords * 4));
 #pragma unroll
-                for (int i = 0; i < kVWords; ++i) v[f][j][i] = p[i];
+                for (int i = 0; i < kVWords; i += kVStep) {
+                    if constexpr (kVStep == 4) {
+                        const u32x4 x = load_cached<STREAM, u32x4>(p + i);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[f][j][i + e] = x[e];
+                    } else if constexpr (kVStep == 2) {
+                        const u32x2 x = load_cached<STREAM, u32x2>(p + i);
+                        v[f][j][i] = x.x;
+                        v[f][j][i + 1] = x.y;
+                    } else {
+                        v[f][j][i] = load_cached<STREAM, unsigned>(p + i);
+                    }
+                }
             }
             if constexpr (E4M3) vs[f] = *reinterpret_cast<const f32x4 *>(a.v_scale + row[f] + kg * 4);
         }
@@ -209,7 +231,8 @@ struct Tile {
     }
 };
 
-template <int D, bool E4M3, int QT>
+// STREAM: the cache is read past the caches.
+template <int D, bool E4M3, int QT, bool STREAM>
 __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     constexpr int kChunks = D / 32;       // 32-value steps of the first product
     constexpr int kVals = D / 16;         // values per lane of V: one MFMA each
@@ -328,7 +351,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     };
     // a tile's K is replaced by the next tile's as soon as the scores are formed,
     // its V once it is transposed, so a wave always has loads in flight
-    Tile<D, E4M3> kv;
+    Tile<D, E4M3, STREAM> kv;
     long long row[2], next[2];
     if (t0 < t1) {
         find_rows(t0, next);
@@ -488,7 +511,9 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             const int rr = i / (D / 4), d = i % (D / 4) * 4;
             const int r = row0 + t * 16 + rr;
             if (r >= rows) break;
-            const float M = fmaxf(fmaxf(sm[0][rr], sm[1][rr]), fmaxf(sm[2][rr], sm[3][rr]));
+            float M = sm[0][rr];
+#pragma unroll
+            for (int v = 1; v < kWavesPerBlock; ++v) M = fmaxf(M, sm[v][rr]);
             float L = 0.0f;
             float4 x = make_float4(0, 0, 0, 0);
 #pragma unroll
@@ -526,70 +551,113 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     }
 }
 
-// One wave per row: the active splits' partials joined.
-template <int D>
+// The active splits' partials of a row joined by JW waves, each taking every JW-th.
+template <int D, int JW>
 __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_rows) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const long long wave = static_cast<long long>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6);
-    const int all = a.N * a.G;
-    if (wave >= static_cast<long long>(a.B) * a.Hkv * all) return;
-    const int r = static_cast<int>(wave % all);
-    const int h = static_cast<int>(wave / all % a.Hkv), b = static_cast<int>(wave / all / a.Hkv);
+    constexpr int kPer = D / kWave;
+    constexpr int kAhead = 4;  // partials a wave loads before it uses one
+    __shared__ float so[JW][D], sl[JW];
+    const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
+    const int all = a.N * a.G, wj = w % JW;
+    const long long unit_row = static_cast<long long>(blockIdx.x) * (kWavesPerBlock / JW) + w / JW;
+    if (unit_row >= static_cast<long long>(a.B) * a.Hkv * all) return;  // JW > 1: a workgroup has one row
+    const int r = static_cast<int>(unit_row % all);
+    const int h = static_cast<int>(unit_row / all % a.Hkv), b = static_cast<int>(unit_row / all / a.Hkv);
     const Span sp = request_span(a, b, lane, nullptr);
     if (!sp.ok || sp.active <= 1 || r >= sp.count * a.G) return;
     const int qb = r / tile_rows;
     const long long unit = ((static_cast<long long>(b) * a.Hkv + h) * a.QB + qb) * a.S;
+    const float *ml = a.part_ml + (unit * tile_rows + r % tile_rows) * 2;
+    const float *po = a.part_o + (unit * tile_rows + r % tile_rows) * D + lane * kPer;
     const float ninf = -__builtin_huge_valf();
     bool bad = false;
     float M = ninf;
     for (int s = lane; s < sp.active; s += kWave) {
         bad |= a.part_bad[unit + s] != 0;
-        M = fmaxf(M, a.part_ml[((unit + s) * tile_rows + r % tile_rows) * 2]);
+        M = fmaxf(M, ml[static_cast<long long>(s) * tile_rows * 2]);
     }
     bad = ballot(bad) != 0;
     M = wave_max(M);
-    float L = 0.0f;
-    constexpr int kPer = D / kWave;
-    float x[kPer] = {};
-    if (M != ninf) {
-#pragma unroll 4
-        for (int s = 0; s < sp.active; ++s) {
-            const long long at = (unit + s) * tile_rows + r % tile_rows;
-            const float ms = a.part_ml[at * 2];
-            const float f = ms == ninf ? 0.0f : fast_exp2((ms - M) * a.c);
-            L += a.part_ml[at * 2 + 1] * f;
+    float L = 0.0f, x[kPer] = {};
+    for (int s0 = wj; s0 < sp.active; s0 += kAhead * JW) {
+        float y[kAhead][kPer], ms[kAhead], ls[kAhead];
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) x[e] += a.part_o[at * D + lane * kPer + e] * f;
+        for (int i = 0; i < kAhead; ++i) {
+            const long long at = static_cast<long long>(min(s0 + i * JW, sp.active - 1)) * tile_rows;
+            ms[i] = ml[at * 2];
+            ls[i] = ml[at * 2 + 1];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) y[i][e] = po[at * D + e];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s0 + i * JW >= sp.active || ms[i] == ninf) continue;
+            const float f = fast_exp2((ms[i] - M) * a.c);
+            L += ls[i] * f;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[e] += y[i][e] * f;
+        }
+    }
+    if constexpr (JW > 1) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) so[w][lane * kPer + e] = x[e];
+        if (lane == 0) sl[w] = L;
+        __syncthreads();
+        if (w != 0) return;
+        L = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int d = lane * kPer + e;
+            x[e] = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
         }
     }
     const long long to = (static_cast<long long>(b) * a.N + r / a.G) * a.H + h * a.G + r % a.G;
     const bool none = bad || M == ninf;
     const float f = none ? 0.0f : 1.0f / L;
+    uint16_t *out = a.out + to * D + lane * kPer;
+    if constexpr (kPer == 1) {
+        *out = none ? 0 : static_cast<uint16_t>(pack_bf16(x[0] * f, 0.0f) & 0xffffu);
+    } else {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-        a.out[to * D + lane * kPer + e] =
-            none ? 0 : static_cast<uint16_t>(pack_bf16(x[e] * f, 0.0f) & 0xffffu);
+        for (int e = 0; e < kPer; e += 2)
+            *reinterpret_cast<unsigned *>(out + e) = none ? 0 : pack_bf16(x[e] * f, x[e + 1] * f);
+    }
     if (lane == 0) {
         if (a.lse) a.lse[to] = none ? ninf : M * a.scale + logf(L);
         if (a.status && h == 0 && r == 0) a.status[b] = bad ? 1 : 0;
     }
 }
 
+template <int D, bool E4M3, int QT>
+hipError_t launch_shape(const AttendArgs &a, dim3 grid, hipStream_t s) {
+    // A cache whose rows one workgroup reads is read past the caches: 346 us
+    // against 375 for 64 requests of one token over 8k (bf16; e4m3 210 and 210, and
+    // plain loads are kept there).  With several row blocks the others find the rows
+    // in the L2: 120 us against 148 for 64 trees of 33.
+    if constexpr (!E4M3)
+        if (a.QB == 1) return launch_kernel(k_attend<D, E4M3, QT, true>, grid, dim3(kBlock), 0, s, a);
+    return launch_kernel(k_attend<D, E4M3, QT, false>, grid, dim3(kBlock), 0, s, a);
+}
+
 template <int D, bool E4M3>
 hipError_t launch_qt(const AttendArgs &a, int QT, dim3 grid, hipStream_t s) {
     if constexpr (D <= 128) {
-        if (QT == 2) return launch_kernel(k_attend<D, E4M3, 2>, grid, dim3(kBlock), 0, s, a);
-        if (QT == 3) return launch_kernel(k_attend<D, E4M3, 3>, grid, dim3(kBlock), 0, s, a);
+        if (QT == 2) return launch_shape<D, E4M3, 2>(a, grid, s);
+        if (QT == 3) return launch_shape<D, E4M3, 3>(a, grid, s);
     }
     if constexpr (D == 64)
-        if (QT == 4) return launch_kernel(k_attend<D, E4M3, 4>, grid, dim3(kBlock), 0, s, a);
-    return launch_kernel(k_attend<D, E4M3, 1>, grid, dim3(kBlock), 0, s, a);
+        if (QT == 4) return launch_shape<D, E4M3, 4>(a, grid, s);
+    return launch_shape<D, E4M3, 1>(a, grid, s);
 }
 
 }  // namespace
 
+// The split.  A wave's run is at most kRun tiles per row tile it holds (8: 1024
+// slots per workgroup; its 2.4 us of preparation are then 6% of its time, and a
+// partial is a small part of what it read), and short enough that about
+// kTargetGroups workgroups share the work, but not below a least run.
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size) {
-    constexpr int kTargetGroups = 1024;  // workgroups a call aims for
+    constexpr int kTargetGroups = 1024, kRun = 8;
     AttendPlan p;
     const int rows = N * (H / Hkv), tiles = (rows + 15) / 16;
     const int most = D == 64 ? 4 : (D == 128 ? 3 : 1);  // row tiles whose accumulators a wave can hold
@@ -599,8 +667,8 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     const long long slots = static_cast<long long>(P) * page_size;
     const long long all = (slots + kTile - 1) / kTile, groups = static_cast<long long>(B) * Hkv * p.QB;
     const long long cap = (all + kWavesPerBlock * p.min_tiles - 1) / (kWavesPerBlock * p.min_tiles);
-    long long want = (kTargetGroups + groups - 1) / groups;
-    want = std::max(want, (all + kWavesPerBlock * 8 - 1) / (kWavesPerBlock * 8));  // 1024 slots per workgroup
+    const long long run = kWavesPerBlock * kRun * p.QT;
+    const long long want = std::max((kTargetGroups + groups - 1) / groups, (all + run - 1) / run);
     p.S = static_cast<int>(std::max(1LL, std::min({want, cap, 1024LL})));
     const size_t units = static_cast<size_t>(groups) * p.S, n = units * p.QT * 16;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
@@ -619,13 +687,23 @@ hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, int QT, hipStrea
     return e4m3 ? launch_qt<256, true>(a, QT, grid, s) : launch_qt<256, false>(a, QT, grid, s);
 }
 
+namespace {
+template <int D>
+hipError_t launch_join(const AttendArgs &a, int tile_rows, hipStream_t s) {
+    const long long rows = static_cast<long long>(a.B) * a.Hkv * a.N * a.G;
+    // few rows, of many splits each as a rule: four waves a row (160 rows of 128
+    // splits 9 us against 17); many: a wave a row (8192 rows of 2 splits 7 against 19)
+    if (rows <= 2048)
+        return launch_kernel(k_attend_join<D, 4>, dim3(static_cast<unsigned>(rows)), dim3(kBlock), 0, s, a, tile_rows);
+    return launch_kernel(k_attend_join<D, 1>, dim3(static_cast<unsigned>((rows + kWavesPerBlock - 1) / kWavesPerBlock)),
+                         dim3(kBlock), 0, s, a, tile_rows);
+}
+}  // namespace
+
 hipError_t launch_attend_join(const AttendArgs &a, int D, int QT, hipStream_t s) {
-    const long long waves = static_cast<long long>(a.B) * a.Hkv * a.N * a.G;
-    const dim3 grid(static_cast<unsigned>((waves + kWavesPerBlock - 1) / kWavesPerBlock));
-    const int rows = QT * 16;
-    if (D == 64) return launch_kernel(k_attend_join<64>, grid, dim3(kBlock), 0, s, a, rows);
-    if (D == 128) return launch_kernel(k_attend_join<128>, grid, dim3(kBlock), 0, s, a, rows);
-    return launch_kernel(k_attend_join<256>, grid, dim3(kBlock), 0, s, a, rows);
+    if (D == 64) return launch_join<64>(a, QT * 16, s);
+    if (D == 128) return launch_join<128>(a, QT * 16, s);
+    return launch_join<256>(a, QT * 16, s);
 }
 
 }  // namespace sv
