@@ -826,9 +826,9 @@ sv_status spec_attend_paged(const void *q, long long q_stride, sv_paged_kv cache
     a.part_bad = reinterpret_cast<int32_t *>(ws + p.part_bad);
     if (!isfinite(a.c)) return SV_ERR_UNSUPPORTED;
     const bool e4m3 = cache.dt == SV_E4M3;
-    hipError_t e = traced(SV_K_ATTEND, stream, [&] { return launch_attend(a, D, e4m3, p.QT, stream); });
+    hipError_t e = traced(SV_K_ATTEND, stream, [&] { return launch_attend(a, D, e4m3, p, stream); });
     if (e == hipSuccess && p.S > 1)
-        e = traced(SV_K_ATTEND_JOIN, stream, [&] { return launch_attend_join(a, D, p.QT, stream); });
+        e = traced(SV_K_ATTEND_JOIN, stream, [&] { return launch_attend_join(a, D, p, stream); });
     return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

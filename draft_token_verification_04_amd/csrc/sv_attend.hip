@@ -26,12 +26,21 @@
 // accumulator, maximum and sum is fp32.  An e4m3 cache is widened to bf16 in
 // registers (exact); its per-row scales multiply the scores and the weights.
 //
-// Work split: the slots of a (request, KV head) go to `active` of S
-// workgroups, each of whose 4 waves takes a run of tiles; a workgroup joins
-// its waves through LDS and writes either the result (one active split) or a
-// partial (m, l, O) that k_attend_join joins.  S comes from the table's size
-// on the host, the runs from the request's own length on the device, so a
-// captured graph replays with other lengths.
+// Work split.  Few rows (kCached, kStream): the slots of a (request, KV head) go
+// to `active` of S workgroups, each of whose 4 waves takes a run of tiles with
+// the next tile's rows in flight, and joins them through LDS.  Many rows
+// (kShared): the waves of a workgroup hold different rows and walk the same
+// tiles, which come through a ring of four stages in LDS, loaded three ahead
+// straight from the pages.  Either way a workgroup writes the result (one active
+// split) or a partial (reference, l, O) that k_attend_join joins.  S comes from
+// the table's size on the host, the runs from the request's own length on the
+// device, so a captured graph replays with other lengths.
+//
+// Bounds and figures (MI355X, 32 query and 8 KV heads of 128): one token, 64
+// requests of 8192: 346 us, 6.2 TB/s of cache, bound by memory; lengths 64..8192:
+// 170 us, 5.5 TB/s, the rest the tail of the longest; e4m3: 5.3 TB/s, half the
+// bytes in flight per wave; 64 trees of 33: 104 us, bound by a tile's chain of
+// LDS reads, products and exponentials with two waves per SIMD (registers).
 //
 // Masked slots: scores are replaced, never added to; value rows behind the
 // last token are zeroed; and a non-finite value of a window token is left to
@@ -44,8 +53,19 @@
 namespace sv {
 namespace {
 
+#define SV_LDS __attribute__((address_space(3)))
+#define SV_GLOBAL __attribute__((address_space(1)))
+
 constexpr int kTile = 32;  // slots a wave takes per step
 constexpr float kSlack = 8.0f;
+// The reference of a row that has met no score (log2 units; a score so low, in
+// these units, would read as masked).  2^(kNoRef - any reference) is 0.
+constexpr float kNoRef = -1e30f;
+
+// Natural log of L 2^ref.
+__device__ __forceinline__ float log_sum(float ref, float L) {
+    return static_cast<float>((static_cast<double>(ref) + static_cast<double>(log2f(L))) * 0.6931471805599453);
+}
 
 __device__ __forceinline__ f32x4 mfma16(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -104,9 +124,10 @@ __device__ __forceinline__ Span request_span(const AttendArgs &a, int b, int lan
     }
     s.total = s.ok ? static_cast<int>(total) : 0;
     s.tiles = (s.total + kTile - 1) / kTile;
-    const int most = a.S * kWavesPerBlock;
-    s.per_wave = max(a.min_tiles, (s.tiles + most - 1) / most);
-    const int per_split = s.per_wave * kWavesPerBlock;
+    // as many splits as have a least run, of equal runs
+    const int splits = max(1, min(a.S, s.tiles / (a.min_tiles * kWavesPerBlock)));
+    s.per_wave = (s.tiles + splits * kWavesPerBlock - 1) / (splits * kWavesPerBlock);
+    const int per_split = max(1, s.per_wave) * kWavesPerBlock;
     s.active = (s.tiles + per_split - 1) / per_split;
     return s;
 }
@@ -156,6 +177,7 @@ __device__ __forceinline__ T load_cached(const void *p) {
 template <int D, bool E4M3, bool STREAM>
 struct Tile {
     static constexpr int kElem = E4M3 ? 1 : 2;
+    static constexpr int kRowB = D * kElem;
     static constexpr int kKVecs = D * kElem / 64;      // 16-byte loads of a K row per lane
     static constexpr int kVWords = D * kElem / 64;     // words of a V row per lane (D / 16 values)
     static constexpr int kVStep = kVWords < 4 ? kVWords : 4;
@@ -198,6 +220,69 @@ struct Tile {
             if constexpr (E4M3) vs[f] = *reinterpret_cast<const f32x4 *>(a.v_scale + row[f] + kg * 4);
         }
     }
+    // The same from a stage of the ring (below): K from the four addresses ka, V
+    // from va, each with the second half's rows 16 rows further.  Each block waits
+    // for its own reads, so nothing is used before it has arrived.
+    __device__ __forceinline__ void read_k(const uint32_t (&ka)[kKVecs], uint32_t stage) {
+        if constexpr (kKVecs == 4)
+            asm volatile(
+                "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+                "ds_read_b128 %4, %8 offset:%12\n\tds_read_b128 %5, %9 offset:%12\n\t"
+                "ds_read_b128 %6, %10 offset:%12\n\tds_read_b128 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
+                : "=&v"(k[0][0]), "=&v"(k[0][1]), "=&v"(k[0][2]), "=&v"(k[0][3]), "=&v"(k[1][0]), "=&v"(k[1][1]),
+                  "=&v"(k[1][2]), "=&v"(k[1][3])
+                : "v"(ka[0] + stage), "v"(ka[1] + stage), "v"(ka[2] + stage), "v"(ka[3] + stage), "i"(16 * kRowB));
+        else if constexpr (kKVecs == 2)
+            asm volatile(
+                "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:%6\n\t"
+                "ds_read_b128 %3, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+                : "=&v"(k[0][0]), "=&v"(k[0][1]), "=&v"(k[1][0]), "=&v"(k[1][1])
+                : "v"(ka[0] + stage), "v"(ka[1] + stage), "i"(16 * kRowB));
+        else
+            asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(k[0][0]), "=&v"(k[1][0])
+                         : "v"(ka[0] + stage), "i"(16 * kRowB));
+    }
+    __device__ __forceinline__ void read_v(const uint32_t (&va)[4], uint32_t stage) {
+#define SV_READ_V(OP, X)                                                                                        \
+    asm volatile(OP " %0, %8 offset:%12\n\t" OP " %1, %9 offset:%12\n\t" OP " %2, %10 offset:%12\n\t" OP          \
+                    " %3, %11 offset:%12\n\t" OP " %4, %8 offset:%13\n\t" OP " %5, %9 offset:%13\n\t" OP          \
+                    " %6, %10 offset:%13\n\t" OP " %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"                   \
+                 : "=&v"(X[0]), "=&v"(X[1]), "=&v"(X[2]), "=&v"(X[3]), "=&v"(X[4]), "=&v"(X[5]), "=&v"(X[6]),     \
+                   "=&v"(X[7])                                                                                   \
+                 : "v"(va[0] + stage), "v"(va[1] + stage), "v"(va[2] + stage), "v"(va[3] + stage),                \
+                   "i"(32 * kRowB), "i"(48 * kRowB))
+        if constexpr (kVWords == 4) {
+            u32x4 x[8];
+            SV_READ_V("ds_read_b128", x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[e / 4][e % 4][i] = x[e][i];
+        } else if constexpr (kVWords == 2) {
+            u32x2 x[8];
+            SV_READ_V("ds_read_b64", x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e / 4][e % 4][0] = x[e].x;
+                v[e / 4][e % 4][1] = x[e].y;
+            }
+        } else {
+            unsigned x[8];
+            SV_READ_V("ds_read_b32", x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e / 4][e % 4][0] = x[e];
+        }
+#undef SV_READ_V
+    }
+    // e4m3: the scales of the scores' rows, 4 kg .. 4 kg + 3 of each half.
+    __device__ __forceinline__ void read_scales(uint32_t at) {
+        asm volatile(
+            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:64\n\tds_read_b128 %2, %4 offset:128\n\t"
+            "ds_read_b128 %3, %4 offset:192\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(ks[0]), "=&v"(ks[1]), "=&v"(vs[0]), "=&v"(vs[1])
+            : "v"(at));
+    }
     // The left operand of the 32 values of step c of the first product.
     __device__ __forceinline__ bf16x8 k_slice(int f, int c) const {
         if constexpr (E4M3)
@@ -231,21 +316,53 @@ struct Tile {
     }
 };
 
-// STREAM: the cache is read past the caches.
-template <int D, bool E4M3, int QT, bool STREAM>
+// How a workgroup's waves divide its work and how the cache reaches them.
+enum AttendMode {
+    kCached,  // the slots are divided; each wave loads its own into registers
+    kStream,  // the same, past the caches
+    kShared   // the rows are divided; all waves walk the same slots through LDS
+};
+
+// The ring of kShared: kStages stages of one tile each, K's 32 rows, V's, and for
+// e4m3 a copy of the tile's 64 scales for each wave, written by global-to-LDS
+// loads of 16 bytes per lane (4 for the scales).  Chunk c of row r lies at place
+// c ^ swizzle(r) of its row, so that the 16 rows of a K slice, a row length
+// apart, lie in different banks.
+template <int D, bool E4M3>
+struct Ring {
+    static constexpr int kRowB = D * (E4M3 ? 1 : 2), kRowChunks = kRowB / 16;
+    static constexpr int kStages = 4;
+    static constexpr int kPieces = 64 * kRowB / 1024;         // 1 KB loads per tile
+    static constexpr int kPerWave = kPieces / kWavesPerBlock;
+    static constexpr int kLoads = kPerWave + (E4M3 ? 1 : 0);  // a wave's loads per tile
+    static constexpr int kStageB = 64 * kRowB + (E4M3 ? kWavesPerBlock * 256 : 0);
+    static __device__ __forceinline__ int swizzle(int r) {
+        return (r / (16 / kRowChunks)) & (kRowChunks - 1);
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // all but the wave's N youngest
+    asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
+
+template <int D, bool E4M3, int QT, AttendMode MODE>
 __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     constexpr int kChunks = D / 32;       // 32-value steps of the first product
     constexpr int kVals = D / 16;         // values per lane of V: one MFMA each
-    constexpr bool kQInLds = QT > 1 || D == 256;
+    constexpr bool kShares = MODE == kShared;
+    constexpr bool kQInLds = !kShares && (QT > 1 || D == 256);
+    constexpr int kRowsPerGroup = QT * 16 * (kShares ? kWavesPerBlock : 1);
     // where the registers just suffice, loads and widenings stay where they are
     // written: moved ahead, as the compiler likes to, they spill (64 requests of 33
     // rows, QT = 3: 203 us, and 120 us in place)
-    constexpr bool kTight = QT * D > 256 || D == 256;
+    constexpr bool kTight = QT * D > 256 || D == 256 || kShares;
     constexpr int kPad = 4;
     // the queries during the walk, the four waves' rows at the end
-    __shared__ union {
+    __shared__ __align__(1024) union {
         u32x4 q[kQInLds ? QT : 1][kChunks][kWave];
-        float o[kWavesPerBlock][16][D + kPad];
+        float o[kShares ? 1 : kWavesPerBlock][16][D + kPad];
+        char ring[kShares ? Ring<D, E4M3>::kStages * Ring<D, E4M3>::kStageB : 16];
     } lds;
     __shared__ float sm[kWavesPerBlock][16], sl[kWavesPerBlock][16];
     __shared__ int sbad;
@@ -263,11 +380,12 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     uint64_t anc;
     const Span sp = request_span(a, b, lane, &anc);
     const bool speaks = h == 0 && qb == 0 && split == 0 && threadIdx.x == 0 && a.status;
-    const int rows = sp.count * a.G, row0 = qb * QT * 16;
+    const int rows = sp.count * a.G, group0 = qb * kRowsPerGroup;
+    const int row0 = group0 + (kShares ? w * QT * 16 : 0);  // this wave's first row
     if (!sp.ok || rows == 0) {
         if (split == 0) {  // a malformed request reads as zeros
-            for (int i = threadIdx.x; i < QT * 16 * D; i += kBlock) {
-                const int r = row0 + i / D;
+            for (int i = threadIdx.x; i < kRowsPerGroup * D; i += kBlock) {
+                const int r = group0 + i / D;
                 if (r >= rows) break;
                 const long long to = (static_cast<long long>(b) * a.N + r / a.G) * a.H + h * a.G + r % a.G;
                 a.out[to * D + i % D] = 0;
@@ -314,10 +432,10 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     };
 
     f32x4 o[QT][kVals];
-    float m[QT], l[QT];
+    float ref[QT], l[QT];  // log2 of what the weights are relative to, and their sum
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        m[t] = -__builtin_huge_valf();
+        ref[t] = kNoRef;
         l[t] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVals; ++i) o[t][i] = f32x4{0, 0, 0, 0};
@@ -326,8 +444,8 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     const int32_t *table = a.page_table + static_cast<long long>(b) * a.P;
     const int page_mask = (1 << a.page_shift) - 1;
     bool bad = false;
-    const int t0 = (split * kWavesPerBlock + w) * sp.per_wave;
-    const int t1 = min(t0 + sp.per_wave, sp.tiles);
+    const int t0 = (split * kWavesPerBlock + (kShares ? 0 : w)) * sp.per_wave;
+    const int t1 = min(t0 + sp.per_wave * (kShares ? kWavesPerBlock : 1), sp.tiles);
     int ids = 0;  // lane i: the page of the i-th 16 slots of 32 tiles
     // rows (in units of rows) of the first slots of a tile's two 16-slot halves;
     // tiles are asked for in order
@@ -336,6 +454,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
         if (half0 == 0) {
             const int s = tile * kTile + 16 * lane;
             ids = s < sp.total ? table[s >> a.page_shift] : 0;
+            asm volatile("" : "+v"(ids));  // waited for here, once in 32 tiles, not where it is used
             const bool out = ids < 0 || ids >= a.num_pages;
             bad |= out && s < t1 * kTile;
             if (out) ids = 0;
@@ -349,11 +468,49 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             row[f] = ((static_cast<long long>(page) * a.Hkv + h) << a.page_shift) + (s & page_mask);
         }
     };
-    // a tile's K is replaced by the next tile's as soon as the scores are formed,
-    // its V once it is transposed, so a wave always has loads in flight
-    Tile<D, E4M3, STREAM> kv;
-    long long row[2], next[2];
-    if (t0 < t1) {
+    Tile<D, E4M3, MODE == kStream> kv;
+    // kCached, kStream: a tile's K is replaced by the next tile's as soon as the
+    // scores are formed, its V once it is transposed, so a wave always has loads in
+    // flight.  kShared: every wave loads its pieces of the tile kStages - 1 ahead.
+    long long next[2];
+    using R = Ring<D == 256 ? 128 : D, E4M3>;
+    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS char *)lds.ring));
+    uint32_t ka[kv.kKVecs], va[4];
+    auto issue = [&](int tile) {
+        find_rows(tile, next);
+        char *stage = lds.ring + (tile - t0) % R::kStages * R::kStageB;
+#pragma unroll
+        for (int i = 0; i < R::kPerWave; ++i) {
+            const int piece = i * kWavesPerBlock + w, of = piece % (R::kPieces / 2);
+            const int r = of * (1024 / R::kRowB) + lane / R::kRowChunks;  // the row this lane loads from
+            const char *from = static_cast<const char *>(piece < R::kPieces / 2 ? a.k_pages : a.v_pages) +
+                               next[of / (R::kPieces / 4)] * R::kRowB + (r & 15) * R::kRowB +
+                               ((lane % R::kRowChunks) ^ R::swizzle(r)) * 16;
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from, (SV_LDS void *)(stage + piece * 1024), 16, 0, 0);
+        }
+        if constexpr (E4M3) {
+            const float *from = (lane < 32 ? a.k_scale : a.v_scale) + ((lane & 16) ? next[1] : next[0]) + col;
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from, (SV_LDS void *)(stage + 64 * R::kRowB + w * 256), 4, 0, 0);
+        }
+    };
+    if constexpr (kShares) {
+        const int fk = R::swizzle(col);
+#pragma unroll
+        for (int c = 0; c < kv.kKVecs; ++c) ka[c] = ring + col * R::kRowB + ((4 * c + kg) ^ fk) * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 4 * kg + j, byte = col * kv.kVWords * 4;
+            va[j] = ring + r * R::kRowB + ((byte / 16) ^ R::swizzle(r)) * 16 + byte % 16;
+        }
+        // the queries have arrived before the ring's loads are counted
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) asm volatile("" : "+v"(qr[t][c]));
+#pragma unroll
+        for (int i = 0; i < R::kStages - 1; ++i)
+            if (t0 + i < t1) issue(t0 + i);
+    } else if (t0 < t1) {
         find_rows(t0, next);
         kv.load_k(a, next, col, kg);
         kv.load_v(a, next, col, kg);
@@ -361,9 +518,23 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     for (int tile = t0; tile < t1; ++tile) {
         const int s0 = tile * kTile;
         const bool more = tile + 1 < t1;
-        row[0] = next[0];
-        row[1] = next[1];
-        if (more) find_rows(tile + 1, next);
+        uint32_t stage = 0;
+        if constexpr (kShares) {
+            // this wave's pieces of the tile have arrived, then everybody's; the
+            // barrier also says that the stage of the tile before is free
+            if (t1 - 1 - tile >= R::kStages - 2)
+                wait_loads<R::kLoads *(R::kStages - 2)>();
+            else
+                wait_loads<0>();
+            asm volatile("s_barrier" ::: "memory");
+            if (tile + R::kStages - 1 < t1) issue(tile + R::kStages - 1);
+            if (row0 >= rows) continue;  // a wave without rows only loads
+            stage = static_cast<uint32_t>((tile - t0) % R::kStages * R::kStageB);
+            kv.read_k(ka, stage);
+            if constexpr (E4M3) kv.read_scales(ring + stage + 64 * R::kRowB + w * 256 + kg * 16);
+        } else if (more) {
+            find_rows(tile + 1, next);
+        }
 
         // scores: slot s0 + 16 f + 4 kg + j of row col
         f32x4 sc[QT][2];
@@ -388,7 +559,10 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             }
         }
         if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
-        if (more) kv.load_k(a, next, col, kg);
+        if constexpr (kShares)
+            kv.read_v(va, stage);
+        else if (more)
+            kv.load_k(a, next, col, kg);
         if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
         const bool edge = s0 + kTile > sp.base;  // slots of the window, or behind it
         bool odd = false;                        // a window token has a non-finite value
@@ -418,22 +592,26 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
-            float top = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3]));
-            top = fmaxf(top, fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-            // the reference stays while no weight exceeds 2^kSlack: one exponent more
-            // or less costs fp32 sums and bf16 weights nothing
-            if (ballot((top - m[t]) * a.c > kSlack || m[t] == -__builtin_huge_valf()) != 0) {
-                top = fmaxf(m[t], quad_max(top));
-                const float f = m[t] == -__builtin_huge_valf() ? 0.0f : fast_exp2((m[t] - top) * a.c);
+            // weights relative to 2^ref.  The reference stays while no weight exceeds
+            // 2^kSlack: a few exponents more cost fp32 sums and bf16 weights nothing
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = fmaf(sc[t][e / 4][e % 4], a.c, -ref[t]);
+            const float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+            if (ballot(top > kSlack) != 0) {
+                float most = sc[t][0][0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) most = fmaxf(most, sc[t][e / 4][e % 4]);
+                const float to = fmaxf(ref[t], quad_max(most) * a.c), f = fast_exp2(ref[t] - to);
                 l[t] *= f;
 #pragma unroll
                 for (int i = 0; i < kVals; ++i) o[t][i] *= f;
-                m[t] = top;
-            }
-            const float ref = m[t] == -__builtin_huge_valf() ? 0.0f : m[t] * a.c;
-            float p[8];
+                ref[t] = to;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = fast_exp2(fmaf(sc[t][e / 4][e % 4], a.c, -ref));
+                for (int e = 0; e < 8; ++e) p[e] = fmaf(sc[t][e / 4][e % 4], a.c, -to);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = fast_exp2(p[e]);
             l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
             if constexpr (E4M3) {
 #pragma unroll
@@ -455,12 +633,14 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                 for (int t = 0; t < QT; ++t)
                     o[t][i * kv.kWordVals + e] = mfma16(vt[e], pf[t], o[t][i * kv.kWordVals + e]);
         }
-        if (more) kv.load_v(a, next, col, kg);
+        if (!kShares && more) kv.load_v(a, next, col, kg);
         if (odd) {
             // the non-finite values, one by one, for the rows that see their token
             for (int s = max(s0, sp.base); s < min(s0 + kTile, sp.total); ++s) {
                 const int e = s - s0;
-                const long long at = (row[e / 16] + e % 16) * D;
+                const int page = uniform(table[s >> a.page_shift]);
+                const long long at = ((((page < 0 || page >= a.num_pages ? 0LL : page) * a.Hkv + h) << a.page_shift) +
+                                      (s & page_mask)) * D;
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
                     float mine = 0.0f;
@@ -486,17 +666,61 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
         }
     }
 
+    const long long unit = ((static_cast<long long>(b) * a.Hkv + h) * a.QB + qb) * a.S + split;
+    if constexpr (kShares) {
+        // every wave has its rows' whole result; each has seen every page
+        const int any = ballot(bad) != 0;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            const int r = row0 + t * 16 + col;
+            const float L = quad_sum(l[t]);
+            if (r >= rows) continue;
+            if (sp.active == 1) {
+                const long long to = (static_cast<long long>(b) * a.N + r / a.G) * a.H + h * a.G + r % a.G;
+                const bool none = any || L == 0.0f;
+                const float f = none ? 0.0f : 1.0f / L;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < kVals; i += 4) {
+                        uint2 y = make_uint2(0, 0);
+                        if (!none)
+                            y = make_uint2(pack_bf16(o[t][i][j] * f, o[t][i + 1][j] * f),
+                                           pack_bf16(o[t][i + 2][j] * f, o[t][i + 3][j] * f));
+                        *reinterpret_cast<uint2 *>(a.out + to * D + (kg * 4 + j) * kVals + i) = y;
+                    }
+                if (a.lse && kg == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(ref[t], L);
+            } else {
+                const long long at = unit * kRowsPerGroup + (w * QT + t) * 16 + col;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < kVals; i += 4)
+                        *reinterpret_cast<float4 *>(a.part_o + at * D + (kg * 4 + j) * kVals + i) =
+                            make_float4(o[t][i][j], o[t][i + 1][j], o[t][i + 2][j], o[t][i + 3][j]);
+                if (kg == 0) {
+                    a.part_ml[at * 2] = ref[t];
+                    a.part_ml[at * 2 + 1] = L;
+                }
+            }
+        }
+        if (threadIdx.x == 0) {
+            if (sp.active > 1) a.part_bad[unit] = any;
+            if (speaks && sp.active == 1) a.status[b] = any;
+        }
+        return;
+    }
+
     // join the four waves' rows through LDS, one row tile at a time
     if (threadIdx.x == 0) sbad = 0;
     __syncthreads();
     if (bad) sbad = 1;
-    const long long unit = ((static_cast<long long>(b) * a.Hkv + h) * a.QB + qb) * a.S + split;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         if (t > 0) __syncthreads();
         const float ll = quad_sum(l[t]);
         if (kg == 0) {
-            sm[w][col] = m[t];
+            sm[w][col] = ref[t];
             sl[w][col] = ll;
         }
         // the lane's values: d = (4 kg + j) kVals + i
@@ -518,8 +742,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             float4 x = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int v = 0; v < kWavesPerBlock; ++v) {
-                if (sm[v][rr] == -__builtin_huge_valf()) continue;
-                const float f = fast_exp2((sm[v][rr] - M) * a.c);
+                const float f = fast_exp2(sm[v][rr] - M);
                 L += sl[v][rr] * f;
                 const float4 y = *reinterpret_cast<const float4 *>(&lds.o[v][rr][d]);
                 x.x += y.x * f;
@@ -529,14 +752,14 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             }
             if (sp.active == 1) {
                 const long long to = (static_cast<long long>(b) * a.N + r / a.G) * a.H + h * a.G + r % a.G;
-                const bool none = sbad || M == -__builtin_huge_valf();
+                const bool none = sbad || L == 0.0f;
                 const float f = none ? 0.0f : 1.0f / L;
                 uint2 y = make_uint2(0, 0);
                 if (!none) y = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
                 *reinterpret_cast<uint2 *>(a.out + to * D + d) = y;
-                if (a.lse && d == 0) a.lse[to] = none ? -__builtin_huge_valf() : M * a.scale + logf(L);
+                if (a.lse && d == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(M, L);
             } else {
-                const long long at = unit * (QT * 16) + t * 16 + rr;
+                const long long at = unit * kRowsPerGroup + t * 16 + rr;
                 *reinterpret_cast<float4 *>(a.part_o + at * D + d) = x;
                 if (d == 0) {
                     a.part_ml[at * 2] = M;
@@ -553,7 +776,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
 
 // The active splits' partials of a row joined by JW waves, each taking every JW-th.
 template <int D, int JW>
-__global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_rows) {
+__global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int group_rows) {
     constexpr int kPer = D / kWave;
     constexpr int kAhead = 4;  // partials a wave loads before it uses one
     __shared__ float so[JW][D], sl[JW];
@@ -565,16 +788,16 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_r
     const int h = static_cast<int>(unit_row / all % a.Hkv), b = static_cast<int>(unit_row / all / a.Hkv);
     const Span sp = request_span(a, b, lane, nullptr);
     if (!sp.ok || sp.active <= 1 || r >= sp.count * a.G) return;
-    const int qb = r / tile_rows;
+    const int qb = r / group_rows;
     const long long unit = ((static_cast<long long>(b) * a.Hkv + h) * a.QB + qb) * a.S;
-    const float *ml = a.part_ml + (unit * tile_rows + r % tile_rows) * 2;
-    const float *po = a.part_o + (unit * tile_rows + r % tile_rows) * D + lane * kPer;
+    const float *ml = a.part_ml + (unit * group_rows + r % group_rows) * 2;
+    const float *po = a.part_o + (unit * group_rows + r % group_rows) * D + lane * kPer;
     const float ninf = -__builtin_huge_valf();
     bool bad = false;
-    float M = ninf;
+    float M = kNoRef;
     for (int s = lane; s < sp.active; s += kWave) {
         bad |= a.part_bad[unit + s] != 0;
-        M = fmaxf(M, ml[static_cast<long long>(s) * tile_rows * 2]);
+        M = fmaxf(M, ml[static_cast<long long>(s) * group_rows * 2]);
     }
     bad = ballot(bad) != 0;
     M = wave_max(M);
@@ -583,7 +806,7 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_r
         float y[kAhead][kPer], ms[kAhead], ls[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const long long at = static_cast<long long>(min(s0 + i * JW, sp.active - 1)) * tile_rows;
+            const long long at = static_cast<long long>(min(s0 + i * JW, sp.active - 1)) * group_rows;
             ms[i] = ml[at * 2];
             ls[i] = ml[at * 2 + 1];
 #pragma unroll
@@ -591,8 +814,8 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_r
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (s0 + i * JW >= sp.active || ms[i] == ninf) continue;
-            const float f = fast_exp2((ms[i] - M) * a.c);
+            if (s0 + i * JW >= sp.active) continue;
+            const float f = fast_exp2(ms[i] - M);
             L += ls[i] * f;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) x[e] += y[i][e] * f;
@@ -612,7 +835,7 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_r
         }
     }
     const long long to = (static_cast<long long>(b) * a.N + r / a.G) * a.H + h * a.G + r % a.G;
-    const bool none = bad || M == ninf;
+    const bool none = bad || L == 0.0f;
     const float f = none ? 0.0f : 1.0f / L;
     uint16_t *out = a.out + to * D + lane * kPer;
     if constexpr (kPer == 1) {
@@ -623,54 +846,68 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int tile_r
             *reinterpret_cast<unsigned *>(out + e) = none ? 0 : pack_bf16(x[e] * f, x[e + 1] * f);
     }
     if (lane == 0) {
-        if (a.lse) a.lse[to] = none ? ninf : M * a.scale + logf(L);
+        if (a.lse) a.lse[to] = none ? ninf : log_sum(M, L);
         if (a.status && h == 0 && r == 0) a.status[b] = bad ? 1 : 0;
     }
 }
 
 template <int D, bool E4M3, int QT>
-hipError_t launch_shape(const AttendArgs &a, dim3 grid, hipStream_t s) {
+hipError_t launch_shape(const AttendArgs &a, bool shares, dim3 grid, hipStream_t s) {
+    if constexpr (D <= 128)
+        if (shares) return launch_kernel(k_attend<D, E4M3, QT, kShared>, grid, dim3(kBlock), 0, s, a);
     // A cache whose rows one workgroup reads is read past the caches: 346 us
     // against 375 for 64 requests of one token over 8k (bf16; e4m3 210 and 210, and
-    // plain loads are kept there).  With several row blocks the others find the rows
-    // in the L2: 120 us against 148 for 64 trees of 33.
+    // plain loads are kept there).
     if constexpr (!E4M3)
-        if (a.QB == 1) return launch_kernel(k_attend<D, E4M3, QT, true>, grid, dim3(kBlock), 0, s, a);
-    return launch_kernel(k_attend<D, E4M3, QT, false>, grid, dim3(kBlock), 0, s, a);
+        if (a.QB == 1) return launch_kernel(k_attend<D, E4M3, QT, kStream>, grid, dim3(kBlock), 0, s, a);
+    if constexpr (E4M3 || D == 256) return launch_kernel(k_attend<D, E4M3, QT, kCached>, grid, dim3(kBlock), 0, s, a);
+    return hipErrorInvalidValue;  // D <= 128 has one row block, or shares
 }
 
 template <int D, bool E4M3>
-hipError_t launch_qt(const AttendArgs &a, int QT, dim3 grid, hipStream_t s) {
+hipError_t launch_qt(const AttendArgs &a, int QT, bool shares, dim3 grid, hipStream_t s) {
     if constexpr (D <= 128) {
-        if (QT == 2) return launch_shape<D, E4M3, 2>(a, grid, s);
-        if (QT == 3) return launch_shape<D, E4M3, 3>(a, grid, s);
+        if (QT == 2) return launch_shape<D, E4M3, 2>(a, shares, grid, s);
+        if (QT == 3) return launch_shape<D, E4M3, 3>(a, shares, grid, s);
     }
-    if constexpr (D == 64)
-        if (QT == 4) return launch_shape<D, E4M3, 4>(a, grid, s);
-    return launch_shape<D, E4M3, 1>(a, grid, s);
+    return launch_shape<D, E4M3, 1>(a, shares, grid, s);
 }
 
 }  // namespace
 
-// The split.  A wave's run is at most kRun tiles per row tile it holds (8: 1024
-// slots per workgroup; its 2.4 us of preparation are then 6% of its time, and a
-// partial is a small part of what it read), and short enough that about
-// kTargetGroups workgroups share the work, but not below a least run.
+// The rows.  Up to three row tiles (D = 256: one) a wave holds them all, and the
+// slots are divided.  With more, the workgroup's waves divide the rows and walk
+// the same slots, up to 12 row tiles per workgroup: 64 trees of 33 (9 row tiles,
+// lengths up to 2048) took 114 us as three row blocks that each read the cache,
+// 104 us sharing it; 64 chains of 16 (4 row tiles) over 2k 121 and 109 us.
+//
+// The slots.  A wave that holds all rows runs over at most kRun tiles per row
+// tile (1024 slots per workgroup and row tile: its 2.4 us of preparation are then
+// 6% of its time, and a partial is a small part of what it read), and over fewer
+// where that leaves the card without kTargetGroups workgroups, but not below a
+// least run.  Waves that share the slots make partials as large as what the
+// workgroup reads in 500 slots, so they are split only past kSharedRun tiles, or
+// for fewer than half as many workgroups: splits of 1024 slots took the trees
+// 99 + 24 us where none took 104.
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size) {
-    constexpr int kTargetGroups = 1024, kRun = 8;
+    constexpr int kTargetGroups = 1024, kRun = 8, kSharedRun = 96;
     AttendPlan p;
     const int rows = N * (H / Hkv), tiles = (rows + 15) / 16;
-    const int most = D == 64 ? 4 : (D == 128 ? 3 : 1);  // row tiles whose accumulators a wave can hold
+    p.shares = D <= 128 && tiles > 3;
+    const int most = D == 256 ? 1 : (p.shares ? 12 : 3);  // row tiles per workgroup
     p.QB = (tiles + most - 1) / most;
-    p.QT = (tiles + p.QB - 1) / p.QB;
-    p.min_tiles = p.QT == 1 ? 2 : 4;
+    const int each = (tiles + p.QB - 1) / p.QB;
+    p.QT = p.shares ? (each + kWavesPerBlock - 1) / kWavesPerBlock : each;
+    p.group_rows = p.QT * 16 * (p.shares ? kWavesPerBlock : 1);
+    p.min_tiles = p.shares ? 8 : (p.QT == 1 ? 2 : 4);
     const long long slots = static_cast<long long>(P) * page_size;
     const long long all = (slots + kTile - 1) / kTile, groups = static_cast<long long>(B) * Hkv * p.QB;
     const long long cap = (all + kWavesPerBlock * p.min_tiles - 1) / (kWavesPerBlock * p.min_tiles);
-    const long long run = kWavesPerBlock * kRun * p.QT;
-    const long long want = std::max((kTargetGroups + groups - 1) / groups, (all + run - 1) / run);
+    const long long run = p.shares ? kSharedRun : kWavesPerBlock * kRun * p.QT;
+    const long long target = p.shares ? kTargetGroups / 2 : kTargetGroups;
+    const long long want = std::max((target + groups - 1) / groups, (all + run - 1) / run);
     p.S = static_cast<int>(std::max(1LL, std::min({want, cap, 1024LL})));
-    const size_t units = static_cast<size_t>(groups) * p.S, n = units * p.QT * 16;
+    const size_t units = static_cast<size_t>(groups) * p.S, n = units * p.group_rows;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     p.part_o = 0;
     p.part_ml = up(p.S > 1 ? n * D * sizeof(float) : 0);
@@ -679,31 +916,33 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     return p;
 }
 
-hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, int QT, hipStream_t s) {
+hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan &p, hipStream_t s) {
     const long long rest = static_cast<long long>(a.S) * a.B * a.Hkv;
     const dim3 grid(static_cast<unsigned>((rest + 7) / 8 * 8 * a.QB));
-    if (D == 64) return e4m3 ? launch_qt<64, true>(a, QT, grid, s) : launch_qt<64, false>(a, QT, grid, s);
-    if (D == 128) return e4m3 ? launch_qt<128, true>(a, QT, grid, s) : launch_qt<128, false>(a, QT, grid, s);
-    return e4m3 ? launch_qt<256, true>(a, QT, grid, s) : launch_qt<256, false>(a, QT, grid, s);
+    const int QT = p.QT;
+    const bool sh = p.shares;
+    if (D == 64) return e4m3 ? launch_qt<64, true>(a, QT, sh, grid, s) : launch_qt<64, false>(a, QT, sh, grid, s);
+    if (D == 128) return e4m3 ? launch_qt<128, true>(a, QT, sh, grid, s) : launch_qt<128, false>(a, QT, sh, grid, s);
+    return e4m3 ? launch_qt<256, true>(a, QT, sh, grid, s) : launch_qt<256, false>(a, QT, sh, grid, s);
 }
 
 namespace {
 template <int D>
-hipError_t launch_join(const AttendArgs &a, int tile_rows, hipStream_t s) {
+hipError_t launch_join(const AttendArgs &a, int group_rows, hipStream_t s) {
     const long long rows = static_cast<long long>(a.B) * a.Hkv * a.N * a.G;
     // few rows, of many splits each as a rule: four waves a row (160 rows of 128
     // splits 9 us against 17); many: a wave a row (8192 rows of 2 splits 7 against 19)
     if (rows <= 2048)
-        return launch_kernel(k_attend_join<D, 4>, dim3(static_cast<unsigned>(rows)), dim3(kBlock), 0, s, a, tile_rows);
+        return launch_kernel(k_attend_join<D, 4>, dim3(static_cast<unsigned>(rows)), dim3(kBlock), 0, s, a, group_rows);
     return launch_kernel(k_attend_join<D, 1>, dim3(static_cast<unsigned>((rows + kWavesPerBlock - 1) / kWavesPerBlock)),
-                         dim3(kBlock), 0, s, a, tile_rows);
+                         dim3(kBlock), 0, s, a, group_rows);
 }
 }  // namespace
 
-hipError_t launch_attend_join(const AttendArgs &a, int D, int QT, hipStream_t s) {
-    if (D == 64) return launch_join<64>(a, QT * 16, s);
-    if (D == 128) return launch_join<128>(a, QT * 16, s);
-    return launch_join<256>(a, QT * 16, s);
+hipError_t launch_attend_join(const AttendArgs &a, int D, const AttendPlan &p, hipStream_t s) {
+    if (D == 64) return launch_join<64>(a, p.group_rows, s);
+    if (D == 128) return launch_join<128>(a, p.group_rows, s);
+    return launch_join<256>(a, p.group_rows, s);
 }
 
 }  // namespace sv

@@ -304,10 +304,12 @@ struct AttendArgs {
 };
 struct AttendPlan {
     int QT, QB, S, min_tiles;         // 16-row tiles per wave, row blocks, splits, least tiles per wave
+    bool shares;                      // the waves of a workgroup divide its rows, not its slots
+    int group_rows;                   // rows of a workgroup
     size_t part_o, part_ml, part_bad, total;  // workspace
 };
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size);
-hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, int QT, hipStream_t s);
-hipError_t launch_attend_join(const AttendArgs &a, int D, int QT, hipStream_t s);
+hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan &p, hipStream_t s);
+hipError_t launch_attend_join(const AttendArgs &a, int D, const AttendPlan &p, hipStream_t s);
 
 }  // namespace sv
