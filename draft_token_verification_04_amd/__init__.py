@@ -718,8 +718,9 @@ def spec_append_kv_paged(q, k, v, cache, page_table, base, positions=None, *, q_
         out["status"] = torch.empty((B, N), dtype=torch.int32, device=dev)
     rc = _call(
         torch, lib.spec_append_kv_paged, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
-        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope), rot, max_pos, int(bool(interleaved)), _ptr(positions), base.data_ptr(), _ptr(counts),
-        B, N, H, cache._c, page_table.data_ptr(), page_table.shape[1], out["q"].data_ptr(),
+        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope), rot, max_pos, int(bool(interleaved)),
+        _ptr(positions), base.data_ptr(), _ptr(counts), B, N, H, cache._c, page_table.data_ptr(),
+        page_table.shape[1], out["q"].data_ptr(),
         _ptr(out.get("status")))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_append_kv_paged")
@@ -764,8 +765,9 @@ def spec_attend_paged(q, cache, page_table, base, *, parents=None, counts=None, 
                     workspace)
     rc = _call(
         torch, lib.spec_attend_paged, dev, stream, q.data_ptr(), qs, cache._c, page_table.data_ptr(), P,
-        base.data_ptr(), _ptr(counts), _ptr(parents), B, N, H, float(D ** -0.5 if scale is None else scale), res["out"].data_ptr(), _ptr(res.get("lse")),
-        _ptr(res.get("status")), ws.data_ptr(), ws.numel() * ws.element_size())
+        base.data_ptr(), _ptr(counts), _ptr(parents), B, N, H, float(D ** -0.5 if scale is None else scale),
+        res["out"].data_ptr(), _ptr(res.get("lse")), _ptr(res.get("status")), ws.data_ptr(),
+        ws.numel() * ws.element_size())
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_attend_paged")
     _hold(torch, dev, stream, ws if workspace is None else None, *res.values())
@@ -800,8 +802,8 @@ def spec_commit_tree_kv_paged(pages, page_table, tree_base, commit_base, accept_
     st = torch.empty(B, dtype=torch.int32, device=dev) if status else None
     rc = _call(
         torch, lib.spec_commit_tree_kv_paged, dev, stream, pages.data_ptr(), _ptr(scales), G, num_pages, kv_heads,
-        page_size, D * pages.element_size(), page_table.data_ptr(), P, B, tree_base.data_ptr(), commit_base.data_ptr(), accept_len.data_ptr(),
-        path.data_ptr(), path.shape[1], _ptr(st))
+        page_size, D * pages.element_size(), page_table.data_ptr(), P, B, tree_base.data_ptr(),
+        commit_base.data_ptr(), accept_len.data_ptr(), path.data_ptr(), path.shape[1], _ptr(st))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_commit_tree_kv_paged")
     _hold(torch, dev, stream, st)
@@ -839,8 +841,8 @@ def spec_token_logprobs(logits, tokens=None, *, temperature=1.0, top_k=0, entrop
     ws = _workspace(torch, lib.sv_token_logprobs_workspace_bytes(R, V, dt, top_k), dev, workspace)
     rc = _call(
         torch, lib.spec_token_logprobs, dev, stream, logits.data_ptr(), _ptr(tokens), R, V, dt, float(temperature),
-        top_k, _ptr(out.get("logprob")), _ptr(out.get("entropy")), _ptr(out.get("top_ids")), _ptr(out.get("top_logprobs")),
-        _ptr(out.get("status")), ws.data_ptr(), ws.numel() * ws.element_size())
+        top_k, _ptr(out.get("logprob")), _ptr(out.get("entropy")), _ptr(out.get("top_ids")),
+        _ptr(out.get("top_logprobs")), _ptr(out.get("status")), ws.data_ptr(), ws.numel() * ws.element_size())
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_token_logprobs")
     _hold(torch, dev, stream, ws if workspace is None else None, *out.values())

@@ -8,11 +8,12 @@
 //
 // The query heads that share a KV head and all the window's tokens form the
 // rows of one product: rows r = n * G + g, 16 to a tile.  A wave walks 32
-// slots at a time, with nothing in LDS:
+// slots at a time:
 //   S^T = K Q^T   (16x16x32 MFMAs; K is the left operand: its rows are 16
 //                  slots, loaded 16 bytes per lane straight from the page)
-//   online softmax; lane l holds 8 slots of row l % 16, so the running maximum
-//                  needs two cross-lane swaps and the sum none until the end;
+//   online softmax; lane l holds 8 slots of row l % 16, so the running reference
+//                  needs two cross-lane swaps where it moves and the sum none
+//                  until the end;
 //   O^T += V^T P^T: lane l's 8 weights are exactly the k-slice that MFMA's
 //                  right operand wants from it (the contraction runs over the
 //                  slots in the order (half, lane group, register)), so the
@@ -21,8 +22,8 @@
 //                  lane l loads 16 bytes (8 values) of each of its 8 slots and
 //                  transposes the 8 x 8 block in registers (v_perm), which
 //                  serves 8 MFMAs, MFMA i holding values d = 8 m + i.
-// The weights are rounded to bf16 for the second product (relative 2^-9 each,
-// independent, averaged over the slots); l sums them unrounded, and every
+// The weights are rounded to bf16 for the second product (at most 2^-8 relative
+// each, independent, averaged over the slots); l sums them unrounded, and every
 // accumulator, maximum and sum is fp32.  An e4m3 cache is widened to bf16 in
 // registers (exact); its per-row scales multiply the scores and the weights.
 //
@@ -56,8 +57,8 @@ namespace {
 #define SV_LDS __attribute__((address_space(3)))
 #define SV_GLOBAL __attribute__((address_space(1)))
 
-constexpr int kTile = 32;  // slots a wave takes per step
-constexpr float kSlack = 8.0f;
+constexpr int kTile = 32;          // slots a wave takes per step
+constexpr float kSlack = 8.0f;     // weights may reach 2^kSlack before the reference moves
 // The reference of a row that has met no score (log2 units; a score so low, in
 // these units, would read as masked).  2^(kNoRef - any reference) is 0.
 constexpr float kNoRef = -1e30f;
