@@ -821,6 +821,7 @@ sv_status spec_attend_paged(const void *q, long long q_stride, sv_paged_kv cache
     a.S = p.S;
     a.QB = p.QB;
     a.min_tiles = p.min_tiles;
+    a.falling = p.falling;
     a.part_o = reinterpret_cast<float *>(ws + p.part_o);
     a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
     a.part_bad = reinterpret_cast<int32_t *>(ws + p.part_bad);

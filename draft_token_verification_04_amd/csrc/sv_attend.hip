@@ -88,7 +88,7 @@ __device__ __forceinline__ float quad_sum(float v) {
 
 // What every workgroup of a request derives from the request's length alike.
 struct Span {
-    int base, count, total, tiles, per_wave, active;
+    int base, count, total, tiles, active;
     bool ok;  // the window lies inside the table and its parent array is well formed
 };
 __device__ __forceinline__ Span request_span(const AttendArgs &a, int b, int lane, uint64_t *anc) {
@@ -125,12 +125,20 @@ __device__ __forceinline__ Span request_span(const AttendArgs &a, int b, int lan
     }
     s.total = s.ok ? static_cast<int>(total) : 0;
     s.tiles = (s.total + kTile - 1) / kTile;
-    // as many splits as have a least run, of equal runs
-    const int splits = max(1, min(a.S, s.tiles / (a.min_tiles * kWavesPerBlock)));
-    s.per_wave = (s.tiles + splits * kWavesPerBlock - 1) / (splits * kWavesPerBlock);
-    const int per_split = max(1, s.per_wave) * kWavesPerBlock;
-    s.active = (s.tiles + per_split - 1) / per_split;
+    // as many splits as have a least run
+    s.active = s.tiles == 0 ? 0 : max(1, min(a.S, s.tiles / (a.min_tiles * kWavesPerBlock)));
     return s;
+}
+
+// First tile of split i of a request.  Where the workgroups come in many rounds
+// (falling), split i's share falls evenly from 3/2 of the mean for the first to
+// 1/2 for the last: workgroups start in the order of i, so the last to start are
+// short and the card drains evenly.  In one round the shares are equal.
+__device__ __forceinline__ int first_tile(const Span &s, int i, bool falling) {
+    const long long n = s.active;
+    if (!falling || n < 2) return static_cast<int>(s.tiles * static_cast<long long>(i) / n);
+    // share of split k: 3 (n - 1) - 2 k of n times 2 (n - 1)
+    return static_cast<int>(s.tiles * (3 * (n - 1) * i - static_cast<long long>(i) * (i - 1)) / (2 * n * (n - 1)));
 }
 
 // The 8 bf16 values of 16 bytes, or of 8 e4m3 bytes.
@@ -445,8 +453,9 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     const int32_t *table = a.page_table + static_cast<long long>(b) * a.P;
     const int page_mask = (1 << a.page_shift) - 1;
     bool bad = false;
-    const int t0 = (split * kWavesPerBlock + (kShares ? 0 : w)) * sp.per_wave;
-    const int t1 = min(t0 + sp.per_wave * (kShares ? kWavesPerBlock : 1), sp.tiles);
+    const int c0 = first_tile(sp, split, a.falling), c1 = first_tile(sp, split + 1, a.falling);
+    const int run = kShares ? c1 - c0 : (c1 - c0 + kWavesPerBlock - 1) / kWavesPerBlock;
+    const int t0 = c0 + (kShares ? 0 : w * run), t1 = min(t0 + run, c1);
     int ids = 0;  // lane i: the page of the i-th 16 slots of 32 tiles
     // rows (in units of rows) of the first slots of a tile's two 16-slot halves;
     // tiles are asked for in order
@@ -885,13 +894,15 @@ hipError_t launch_qt(const AttendArgs &a, int QT, bool shares, dim3 grid, hipStr
 // The slots.  A wave that holds all rows runs over at most kRun tiles per row
 // tile (1024 slots per workgroup and row tile: its 2.4 us of preparation are then
 // 6% of its time, and a partial is a small part of what it read), and over fewer
-// where that leaves the card without kTargetGroups workgroups, but not below a
-// least run.  Waves that share the slots make partials as large as what the
-// workgroup reads in 500 slots, so they are split only past kSharedRun tiles, or
-// for fewer than half as many workgroups: splits of 1024 slots took the trees
-// 99 + 24 us where none took 104.
+// where that leaves the card without kTargetGroups workgroups (two per compute
+// unit, what the registers of two row tiles admit: 1024 took one chain of 5 over
+// 128k 97 + 10 us where 512 take 90 + 6, and 64 chains of 8 over 2k 103 + 13 where
+// one split takes 91), but not below a least run.  Waves that share the slots make
+// partials as large as what the workgroup reads in 500 slots, so they are split
+// only past kSharedRun tiles or for want of workgroups: splits of 1024 slots took
+// the trees 99 + 24 us where none took 104.
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size) {
-    constexpr int kTargetGroups = 1024, kRun = 8, kSharedRun = 96;
+    constexpr int kTargetGroups = 512, kRun = 8, kSharedRun = 96;
     AttendPlan p;
     const int rows = N * (H / Hkv), tiles = (rows + 15) / 16;
     p.shares = D <= 128 && tiles > 3;
@@ -905,9 +916,9 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     const long long all = (slots + kTile - 1) / kTile, groups = static_cast<long long>(B) * Hkv * p.QB;
     const long long cap = (all + kWavesPerBlock * p.min_tiles - 1) / (kWavesPerBlock * p.min_tiles);
     const long long run = p.shares ? kSharedRun : kWavesPerBlock * kRun * p.QT;
-    const long long target = p.shares ? kTargetGroups / 2 : kTargetGroups;
-    const long long want = std::max((target + groups - 1) / groups, (all + run - 1) / run);
+    const long long want = std::max((kTargetGroups + groups - 1) / groups, (all + run - 1) / run);
     p.S = static_cast<int>(std::max(1LL, std::min({want, cap, 1024LL})));
+    p.falling = groups * p.S >= 4 * kTargetGroups;
     const size_t units = static_cast<size_t>(groups) * p.S, n = units * p.group_rows;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     p.part_o = 0;

@@ -299,12 +299,14 @@ struct AttendArgs {
     float *lse;              // [B][N][H] or null
     int32_t *status;         // [B] or null
     int S, QB, min_tiles;    // splits, row blocks, least tiles per wave
+    bool falling;            // splits of falling size
     float *part_o, *part_ml; // [B][Hkv][QB][S][rows] x D, x 2
     int32_t *part_bad;       // [B][Hkv][QB][S]
 };
 struct AttendPlan {
     int QT, QB, S, min_tiles;         // 16-row tiles per wave, row blocks, splits, least tiles per wave
     bool shares;                      // the waves of a workgroup divide its rows, not its slots
+    bool falling;                     // splits of falling size
     int group_rows;                   // rows of a workgroup
     size_t part_o, part_ml, part_bad, total;  // workspace
 };
