@@ -916,7 +916,9 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     const long long all = (slots + kTile - 1) / kTile, groups = static_cast<long long>(B) * Hkv * p.QB;
     const long long cap = (all + kWavesPerBlock * p.min_tiles - 1) / (kWavesPerBlock * p.min_tiles);
     const long long run = p.shares ? kSharedRun : kWavesPerBlock * kRun * p.QT;
-    const long long want = std::max((kTargetGroups + groups - 1) / groups, (all + run - 1) / run);
+    long long want = std::max((kTargetGroups + groups - 1) / groups, (all + run - 1) / run);
+    if (groups * want < 4 * kTargetGroups)  // whole rounds of the card: a part of one takes as long
+        want = std::max(want, (groups * want + kTargetGroups - 1) / kTargetGroups * kTargetGroups / groups);
     p.S = static_cast<int>(std::max(1LL, std::min({want, cap, 1024LL})));
     p.falling = groups * p.S >= 4 * kTargetGroups;
     const size_t units = static_cast<size_t>(groups) * p.S, n = units * p.group_rows;
