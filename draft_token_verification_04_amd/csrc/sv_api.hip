@@ -10,6 +10,7 @@
 
 #include "sv_device.hpp"
 #include "sv_internal.hpp"
+#include "sv_paged_internal.hpp"
 #include "sv_skip.hpp"
 
 namespace sv {

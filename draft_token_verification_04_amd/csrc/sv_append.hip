@@ -17,8 +17,8 @@
 // the maximum and the half-split rotation's partners move between the lanes of
 // a row.  A workgroup takes one token: its lanes keep the token's angles in
 // registers over all the rows they walk.
-#include "sv_internal.hpp"
 #include "sv_paged.hpp"
+#include "sv_paged_internal.hpp"
 
 namespace sv {
 namespace {

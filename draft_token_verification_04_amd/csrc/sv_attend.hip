@@ -48,8 +48,8 @@
 // the rows that see the token (0 * inf would reach the others).
 #include <algorithm>
 
-#include "sv_internal.hpp"
 #include "sv_paged.hpp"
+#include "sv_paged_internal.hpp"
 
 namespace sv {
 namespace {

@@ -32,8 +32,8 @@
 // groups whose ties come later.
 #include <algorithm>
 
-#include "sv_internal.hpp"
 #include "sv_paged.hpp"
+#include "sv_paged_internal.hpp"
 
 namespace sv {
 namespace {
