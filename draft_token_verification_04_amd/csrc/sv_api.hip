@@ -662,6 +662,9 @@ sv_status spec_commit_tree_kv(const void *src_kv, void *dst_kv, int G, int B, in
 
 namespace {
 
+// Slots of a page table: sums of a slot and a tile or a wave's reach stay in an int.
+constexpr long long kMaxSlots = 1LL << 30;
+
 bool power_of_two(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
 bool paged_sizes_ok(int page_size, int head_dim) {
@@ -673,7 +676,7 @@ bool paged_sizes_ok(int page_size, int head_dim) {
 sv_status check_cache(const sv_paged_kv &c, int P) {
     if (c.dt != SV_BF16 && c.dt != SV_E4M3) return SV_ERR_UNSUPPORTED;
     if (c.num_pages < 1 || c.kv_heads < 1 || c.page_size < 1 || c.head_dim < 1 || P < 1) return SV_ERR_INVALID_ARG;
-    if (!paged_sizes_ok(c.page_size, c.head_dim) || static_cast<long long>(P) * c.page_size > 0x7fffffffLL)
+    if (!paged_sizes_ok(c.page_size, c.head_dim) || static_cast<long long>(P) * c.page_size > kMaxSlots)
         return SV_ERR_UNSUPPORTED;
     const double bytes = static_cast<double>(c.num_pages) * c.kv_heads * c.page_size * c.head_dim;
     if (bytes >= 4.0e18) return SV_ERR_UNSUPPORTED;
@@ -687,7 +690,7 @@ sv_status check_cache_pointers(const sv_paged_kv &c) {
 }
 
 bool attend_sizes_ok(int B, int N, int H, int kv_heads, int head_dim, int P, int page_size) {
-    if (!paged_sizes_ok(page_size, head_dim) || static_cast<long long>(P) * page_size > 0x7fffffffLL) return false;
+    if (!paged_sizes_ok(page_size, head_dim) || static_cast<long long>(P) * page_size > kMaxSlots) return false;
     if (N > SV_MAX_WINDOW || H > 65536 || static_cast<double>(B) * N * H > 2.0e9) return false;
     if (B == 0) return true;
     const AttendPlan p = attend_plan(B, N, H, kv_heads, head_dim, P, page_size);
@@ -843,7 +846,7 @@ sv_status spec_commit_tree_kv_paged(void *pages, float *scales, int G, int num_p
         row_bytes % 16 != 0)
         return SV_ERR_INVALID_ARG;
     if (!power_of_two(page_size) || page_size < 16 || page_size > 1024 || !power_of_two(row_bytes) ||
-        row_bytes > 1024 || N > SV_MAX_TREE_NODES || kv_heads > 32768 || static_cast<long long>(P) * page_size > 0x7fffffffLL ||
+        row_bytes > 1024 || N > SV_MAX_TREE_NODES || kv_heads > 32768 || static_cast<long long>(P) * page_size > kMaxSlots ||
         static_cast<double>(G) * B * kv_heads > 2.0e9)
         return SV_ERR_UNSUPPORTED;
     if (static_cast<double>(G) * num_pages * kv_heads * page_size * row_bytes >= 9.0e18) return SV_ERR_UNSUPPORTED;

@@ -353,7 +353,7 @@ sv_status spec_ngram_candidates(const int32_t *context, int B, int L, const int3
  *   SV_ERR_UNSUPPORTED), num_pages and kv_heads at least 1.
  * Slot s of request b is row s % page_size of page page_table[b][s / page_size],
  * page_table [B][P] int32 on the device.  Page ids are checked before they are
- * used as addresses.  P * page_size must be below 2^31 (else
+ * used as addresses.  P * page_size must be at most 2^30 (else
  * SV_ERR_UNSUPPORTED); offsets into the cache are 64-bit.
  *
  * A request's cached tokens fill its slots from 0; a window of N new tokens
@@ -428,6 +428,7 @@ sv_status spec_append_kv_paged(const void *q, const void *k, const void *v, long
  *     page outside the cache; 2 the parent array is malformed.  The rows of a
  *     request with a non-zero status are 0, their lse -inf.
  * Weights are rounded to bf16 for the second product; sums and maxima are fp32.
+ * Scores (scale q.k) must lie within +-1e29; lower ones read as masked.
  * What a masked slot holds, infinities and NaN included, reaches no row.
  * Workspace: sv_attend_workspace_bytes (0 for invalid or unsupported sizes).
  */

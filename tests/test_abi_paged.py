@@ -49,7 +49,7 @@ def test_append_refusals(lib):
         assert _append(lib, _cache(**c)) == INV, c
     for kw, want in [(dict(B=-1), INV), (dict(N=0), INV), (dict(H=0), INV), (dict(P=0), INV), (dict(eps=-1.0), INV),
                      (dict(eps=float("nan")), INV), (dict(eps=float("inf")), INV), (dict(rot=0), INV),
-                     (dict(rot=144), INV), (dict(rot=24), UNS), (dict(max_pos=0), INV), (dict(P=1 << 28), UNS),
+                     (dict(rot=144), INV), (dict(rot=24), UNS), (dict(max_pos=0), INV), (dict(P=1 << 28), UNS), (dict(P=(1 << 26) + 1), UNS),
                      (dict(B=1 << 20, N=1 << 20), UNS), (dict(H=1 << 17), UNS), (dict(q=None), INV),
                      (dict(k=None), INV), (dict(v=None), INV), (dict(base=None), INV), (dict(table=None), INV),
                      (dict(out=None), INV), (dict(pos=None), INV), (dict(wq=FAKE), INV), (dict(wk=FAKE), INV),
@@ -76,7 +76,7 @@ def test_attend_refusals(lib):
         assert _attend(lib, _cache(**c)) == INV, c
     for kw, want in [(dict(B=-1), INV), (dict(N=0), INV), (dict(H=0), INV), (dict(H=3), INV), (dict(P=0), INV),
                      (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV),
-                     (dict(scale=float("inf")), INV), (dict(N=sv.SV_MAX_WINDOW + 1), UNS), (dict(P=1 << 27), UNS),
+                     (dict(scale=float("inf")), INV), (dict(N=sv.SV_MAX_WINDOW + 1), UNS), (dict(P=1 << 27), UNS), (dict(P=(1 << 26) + 1), UNS),
                      (dict(B=1 << 30), UNS), (dict(H=1 << 18), UNS), (dict(q=None), INV), (dict(table=None), INV),
                      (dict(base=None), INV), (dict(out=None), INV), (dict(ws=None), INV), (dict(q=ODD), INV),
                      (dict(out=ODD), INV), (dict(ws=ODD), INV), (dict(qs=508), INV), (dict(qs=504), INV),
@@ -112,7 +112,8 @@ def test_commit_paged_refusals(lib):
     for kw, want in [(dict(G=0), INV), (dict(B=-1), INV), (dict(np=0), INV), (dict(h=0), INV), (dict(P=0), INV),
                      (dict(N=0), INV), (dict(ps=0), INV), (dict(rb=8), INV), (dict(rb=24), INV), (dict(ps=8), UNS),
                      (dict(ps=40), UNS), (dict(ps=2048), UNS), (dict(rb=48), UNS), (dict(rb=2048), UNS),
-                     (dict(N=sv.SV_MAX_TREE_NODES + 1), UNS), (dict(P=1 << 28), UNS), (dict(G=1 << 20, B=1 << 12), UNS),
+                     (dict(N=sv.SV_MAX_TREE_NODES + 1), UNS), (dict(P=1 << 28), UNS), (dict(P=(1 << 26) + 1), UNS),
+                     (dict(h=32769), UNS), (dict(G=1 << 20, B=1 << 12), UNS),
                      (dict(pages=None), INV), (dict(table=None), INV), (dict(tb=None), INV), (dict(cb=None), INV),
                      (dict(d=None), INV), (dict(p=None), INV), (dict(pages=ODD), INV)]:
         assert _commit(lib, **kw) == want, kw

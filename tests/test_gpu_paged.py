@@ -74,6 +74,55 @@ def test_long_contexts_split_and_join(kind, N):
     check_attend(g, o, 9001)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,H,Hkv,N", [(128, 8, 2, 33), (64, 4, 1, 40), (128, 4, 1, 64)])
+def test_windows_of_many_rows_split_and_join(kind, D, H, Hkv, N):
+    # more rows than a wave holds, over contexts long enough for several splits,
+    # with a bad page in the second request's last split only
+    note(f"attend shared split {kind} D={D} N={N}")
+    rng = np.random.default_rng(N + D)
+    base, counts = np.array([5000, 4000, 0, 1100]), np.array([N, N, N, N - 7])
+    P = -(-(5000 + N) // 32)
+    assert sv.attend_workspace_bytes(4, N, H, Hkv, D, P, 32) > 256
+    table, n = np.zeros((4, P), np.int64), 2 * P + 120
+    ids = rng.permutation(n)
+    for b, used in enumerate((P, P, 4, 40)):
+        table[b, :used], ids = ids[:used], ids[used:]
+    table[1, 3990 // 32] = n
+    cache = Cache(rng, n, Hkv, 32, D, kind)
+    g, o = run_attend(rng, cache, table, base, N, H, counts=counts, parents=random_tree(rng, 4, N))
+    assert o["status"].tolist() == [0, 1, 0, 0]
+    check_attend(g, o, 5000 + N)
+
+
+@pytest.mark.parametrize("D,H,Hkv,N", [(128, 16, 1, 64), (64, 24, 1, 50), (256, 8, 1, 20)])
+def test_windows_of_several_row_blocks(D, H, Hkv, N):
+    note(f"attend row blocks D={D} H={H} N={N}")
+    rng = np.random.default_rng(N + H)
+    table, n = _table(rng, 2, 12)
+    cache = Cache(rng, n, Hkv, 16, D, "bf16")
+    g, o = run_attend(rng, cache, table, np.array([100, 37]), N, H, counts=np.array([N, N - 3]))
+    check_attend(g, o, 100 + N)
+
+
+def test_many_requests_in_many_rounds():
+    # enough workgroups for splits of falling size; a few long requests among short ones
+    note("attend falling splits")
+    rng = np.random.default_rng(29)
+    B, H, Hkv, D, P = 128, 4, 4, 64, 256
+    base = rng.integers(0, 40, B)
+    base[[3, 50, 127]] = [4000, 2500, 4095]
+    table = np.zeros((B, P), np.int64)
+    ids = rng.permutation(3 * P + B * 3)
+    for b in range(B):
+        used = -(-(base[b] + 1) // 16)
+        table[b, :used], ids = ids[:used], ids[used:]
+    cache = Cache(rng, 3 * P + B * 3, Hkv, 16, D, "bf16")
+    g, o = run_attend(rng, cache, table, base, 1, H)
+    assert (o["status"] == 0).all()
+    check_attend(g, o, 4096)
+
+
 def test_scores_far_apart_and_the_scale():
     # one slot takes all the weight, moving from tile to tile; a tiny and a large scale
     note("attend scores far apart")
