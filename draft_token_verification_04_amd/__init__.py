@@ -26,6 +26,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -728,6 +729,7 @@ def spec_append_kv_paged(q, k, v, cache, page_table, base, positions=None, *, q_
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def attend_workspace_bytes(B, N, H, kv_heads, head_dim, P, page_size) -> int:
     return int(load_library().sv_attend_workspace_bytes(B, N, H, kv_heads, head_dim, P, page_size))
 
@@ -761,8 +763,7 @@ def spec_attend_paged(q, cache, page_table, base, *, parents=None, counts=None, 
         res["lse"] = _window_out(torch, None if lse is True else lse, "lse", (B, N, H), torch.float32, dev)
     if status:
         res["status"] = torch.empty(B, dtype=torch.int32, device=dev)
-    ws = _workspace(torch, lib.sv_attend_workspace_bytes(B, N, H, cache.kv_heads, D, P, cache.page_size), dev,
-                    workspace)
+    ws = _workspace(torch, attend_workspace_bytes(B, N, H, cache.kv_heads, D, P, cache.page_size), dev, workspace)
     rc = _call(
         torch, lib.spec_attend_paged, dev, stream, q.data_ptr(), qs, cache._c, page_table.data_ptr(), P,
         base.data_ptr(), _ptr(counts), _ptr(parents), B, N, H, float(D ** -0.5 if scale is None else scale),
@@ -810,6 +811,7 @@ def spec_commit_tree_kv_paged(pages, page_table, tree_base, commit_base, accept_
     return st
 
 
+@functools.lru_cache(maxsize=4096)
 def token_logprobs_workspace_bytes(R, V, dtype_code, top_k) -> int:
     return int(load_library().sv_token_logprobs_workspace_bytes(R, V, dtype_code, top_k))
 
@@ -838,7 +840,7 @@ def spec_token_logprobs(logits, tokens=None, *, temperature=1.0, top_k=0, entrop
         out["top_logprobs"] = torch.empty((R, max(top_k, 0)), dtype=torch.float32, device=dev)
     if status:
         out["status"] = torch.empty(R, dtype=torch.int32, device=dev)
-    ws = _workspace(torch, lib.sv_token_logprobs_workspace_bytes(R, V, dt, top_k), dev, workspace)
+    ws = _workspace(torch, token_logprobs_workspace_bytes(R, V, dt, top_k), dev, workspace)
     rc = _call(
         torch, lib.spec_token_logprobs, dev, stream, logits.data_ptr(), _ptr(tokens), R, V, dt, float(temperature),
         top_k, _ptr(out.get("logprob")), _ptr(out.get("entropy")), _ptr(out.get("top_ids")),

@@ -22,9 +22,13 @@
 //                  lane l loads 16 bytes (8 values) of each of its 8 slots and
 //                  transposes the 8 x 8 block in registers (v_perm), which
 //                  serves 8 MFMAs, MFMA i holding values d = 8 m + i.
-// The weights are rounded to bf16 for the second product (at most 2^-8 relative
-// each, independent, averaged over the slots); l sums them unrounded, and every
-// accumulator, maximum and sum is fp32.  An e4m3 cache is widened to bf16 in
+// The weights enter the second product as two bf16 terms, the rounded weight and
+// the rounded rest (2^-16 relative): up to two row tiles per wave the products
+// that this adds are hidden behind the cache's bytes.  With three (windows of 33
+// rows per KV head and more), where they are not and the registers are full, it
+// takes the first term alone: at most 2^-8 relative for each weight, independent,
+// averaged over the slots.  l sums the weights unrounded, and every accumulator,
+// reference and sum is fp32.  An e4m3 cache is widened to bf16 in
 // registers (exact); its per-row scales multiply the scores and the weights.
 //
 // Work split.  Few rows (kCached, kStream): the slots of a (request, KV head) go
@@ -366,6 +370,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     // written: moved ahead, as the compiler likes to, they spill (64 requests of 33
     // rows, QT = 3: 203 us, and 120 us in place)
     constexpr bool kTight = QT * D > 256 || D == 256 || kShares;
+    constexpr bool kTwoTerms = QT < 3;  // weights as two bf16 terms, where the registers allow
     constexpr int kPad = 4;
     // the queries during the walk, the four waves' rows at the end
     __shared__ __align__(1024) union {
@@ -598,7 +603,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             odd = ballot(odd) != 0;
         }
 
-        bf16x8 pf[QT];
+        bf16x8 pf[QT], pl[kTwoTerms ? QT : 1];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
@@ -631,6 +636,11 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                 }
             }
             pf[t] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+            if constexpr (kTwoTerms) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] -= static_cast<float>(pf[t][e]);
+                pl[t] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+            }
         }
 #pragma unroll
         for (int i = 0; i < kv.kVWords; ++i) {
@@ -640,8 +650,11 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
 #pragma unroll
             for (int e = 0; e < kv.kWordVals; ++e)
 #pragma unroll
-                for (int t = 0; t < QT; ++t)
-                    o[t][i * kv.kWordVals + e] = mfma16(vt[e], pf[t], o[t][i * kv.kWordVals + e]);
+                for (int t = 0; t < QT; ++t) {
+                    f32x4 &x = o[t][i * kv.kWordVals + e];
+                    x = mfma16(vt[e], pf[t], x);
+                    if constexpr (kTwoTerms) x = mfma16(vt[e], pl[t], x);
+                }
         }
         if (!kShares && more) kv.load_v(a, next, col, kg);
         if (odd) {
