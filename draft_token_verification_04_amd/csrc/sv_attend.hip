@@ -914,8 +914,15 @@ hipError_t launch_qt(const AttendArgs &a, int QT, bool shares, dim3 grid, hipStr
 // partials as large as what the workgroup reads in 500 slots, so they are split
 // only past kSharedRun tiles or for want of workgroups: splits of 1024 slots took
 // the trees 99 + 24 us where none took 104.
+//
+// Two or three row tiles of several requests that have to be split anyway get
+// kFineRun, and shares that fall (first_tile) from two rounds of the card on, since
+// a batch's lengths seldom agree: 32 chains of 8 over lengths up to 4096 took 54 us
+// so and 70 otherwise (e4m3 36 and 43), where all are 4096 long 102 and 93.  With
+// kTargetGroups pairs or more the join takes back what it gains (64 chains of 8
+// over lengths up to 2048: 57 + 9 against 69, all 2048 long 99 + 11 against 91).
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size) {
-    constexpr int kTargetGroups = 512, kRun = 8, kSharedRun = 96;
+    constexpr int kTargetGroups = 512, kRun = 8, kFineRun = 6, kSharedRun = 96;
     AttendPlan p;
     const int rows = N * (H / Hkv), tiles = (rows + 15) / 16;
     p.shares = D <= 128 && tiles > 3;
@@ -928,12 +935,13 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     const long long slots = static_cast<long long>(P) * page_size;
     const long long all = (slots + kTile - 1) / kTile, groups = static_cast<long long>(B) * Hkv * p.QB;
     const long long cap = (all + kWavesPerBlock * p.min_tiles - 1) / (kWavesPerBlock * p.min_tiles);
-    const long long run = p.shares ? kSharedRun : kWavesPerBlock * kRun * p.QT;
+    const bool fine = B > 1 && p.QT > 1 && !p.shares && groups < kTargetGroups;
+    const long long run = p.shares ? kSharedRun : kWavesPerBlock * (fine ? kFineRun : kRun) * p.QT;
     long long want = std::max((kTargetGroups + groups - 1) / groups, (all + run - 1) / run);
     if (groups * want < 4 * kTargetGroups)  // whole rounds of the card: a part of one takes as long
         want = std::max(want, (groups * want + kTargetGroups - 1) / kTargetGroups * kTargetGroups / groups);
     p.S = static_cast<int>(std::max(1LL, std::min({want, cap, 1024LL})));
-    p.falling = groups * p.S >= 4 * kTargetGroups;
+    p.falling = groups * p.S >= (fine ? 2 : 4) * kTargetGroups;
     const size_t units = static_cast<size_t>(groups) * p.S, n = units * p.group_rows;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     p.part_o = 0;

@@ -123,6 +123,26 @@ def test_many_requests_in_many_rounds():
     check_attend(g, o, 4096)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_windows_of_uneven_requests_in_splits_of_falling_size(kind):
+    note(f"attend falling splits of windows {kind}")
+    rng = np.random.default_rng(31)
+    B, N, H, Hkv, D, P = 96, 8, 12, 4, 64, 256
+    base = rng.integers(0, 40, B)
+    base[[2, 40, 95]] = [4088, 1025, 2500]
+    counts = rng.integers(1, N + 1, B)
+    counts[[2, 40]] = N
+    table = np.full((B, P), -1, np.int64)
+    ids = rng.permutation(3 * P + B * 3)
+    for b in range(B):
+        used = -(-(base[b] + counts[b]) // 16)
+        table[b, :used], ids = ids[:used], ids[used:]
+    cache = Cache(rng, 3 * P + B * 3, Hkv, 16, D, kind)
+    g, o = run_attend(rng, cache, table, base, N, H, counts=counts)
+    assert (o["status"] == 0).all()
+    check_attend(g, o, 4096)
+
+
 def test_scores_far_apart_and_the_scale():
     # one slot takes all the weight, moving from tile to tile; a tiny and a large scale
     note("attend scores far apart")
@@ -134,11 +154,12 @@ def test_scores_far_apart_and_the_scale():
         check_attend(g, o, 304)
 
 
+@pytest.mark.parametrize("H,D", [(4, 128), (16, 128), (32, 128), (24, 64)])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-def test_what_masked_and_unused_slots_hold_reaches_no_row(kind):
-    note(f"attend masked non-finite {kind}")
+def test_what_masked_and_unused_slots_hold_reaches_no_row(kind, H, D):
+    note(f"attend masked non-finite {kind} H={H} D={D}")
     rng = np.random.default_rng(11)
-    B, N, H, Hkv, page, P, D = 4, 9, 4, 2, 16, 6, 128
+    B, N, Hkv, page, P = 4, 9, 2, 16, 6
     base, counts = np.array([0, 5, 40, 55]), np.array([9, 9, 4, 9])
     par = random_tree(rng, B, N)
     par[:, 5] = 2  # tokens 6.. hang off others than 5 in part
