@@ -295,7 +295,10 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
     float *__restrict__ entropy, int32_t *__restrict__ top_ids, float *__restrict__ top_logprobs,
     int32_t *__restrict__ status) {
     constexpr int P = E::kPerVec;
-    constexpr int kHeld = 6;  // segments per wave whose group maxima stay in registers
+    // segments per wave whose group maxima stay in registers, asked for together: few
+    // rows have many segments and nothing but this latency (8 rows of 151936 fp32,
+    // 38 a wave: 6.5 us against 10 with 6 held and the rest in rounds of 8)
+    constexpr int kHeld = U == 4 ? 40 : 6;
     __shared__ __align__(16) uint64_t lists[kWavesPerBlock][kListCap];
     __shared__ float col[kWavesPerBlock][kWave];
     __shared__ float sM[kWavesPerBlock];
@@ -311,10 +314,10 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
     LogprobPart mine = {0.0, 0.0, ninf, 0.0f};
     if (threadIdx.x < segs) mine = pp[threadIdx.x];
     float held[kHeld];
+    if (k) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int s = w + i * kWavesPerBlock;
-        held[i] = k && s < segs ? gm[static_cast<long long>(s) * kWave] : ninf;
+        for (int i = 0; i < kHeld; ++i)
+            held[i] = gm[static_cast<long long>(min(w + i * kWavesPerBlock, segs - 1)) * kWave];
     }
     if (tokens && uniform(tok) == -1) {
         if (threadIdx.x == 0) {
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
     float cm = ninf;
     if (k) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) cm = fmaxf(cm, held[i]);
+        for (int i = 0; i < kHeld; ++i) cm = fmaxf(cm, held[i]);  // the last segment twice: no matter
 #pragma unroll 8
         for (int s = w + kHeld * kWavesPerBlock; s < segs; s += kWavesPerBlock)
             cm = fmaxf(cm, gm[static_cast<long long>(s) * kWave]);

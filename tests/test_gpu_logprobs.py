@@ -70,6 +70,13 @@ def test_sizes(dtype, R, V, k):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,V", [(2, 400001), (32, 262145)])
+def test_rows_of_more_segments_than_the_join_holds(dtype, R, V):
+    note(f"logprobs {dtype} R={R} V={V}")
+    _run(np.random.default_rng(V), R, V, dtype, 1.0, 20)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_at_every_place_on_the_16_byte_grid(dtype):
     # unaligned bases and odd row lengths; what lies around the rows is +inf
     note(f"logprobs alignment {dtype}")
