@@ -44,7 +44,7 @@
 // Bounds and figures (MI355X, 32 query and 8 KV heads of 128): one token, 64
 // requests of 8192: 346 us, 6.2 TB/s of cache, bound by memory; lengths 64..8192:
 // 170 us, 5.5 TB/s, the rest the tail of the longest; e4m3: 5.3 TB/s, half the
-// bytes in flight per wave; 64 trees of 33: 104 us, bound by a tile's chain of
+// bytes in flight per wave; 64 trees of 33: 105 us, bound by a tile's chain of
 // LDS reads, products and exponentials with two waves per SIMD (registers).
 //
 // Masked slots: scores are replaced, never added to; value rows behind the
@@ -395,7 +395,11 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     const Span sp = request_span(a, b, lane, &anc);
     const bool speaks = h == 0 && qb == 0 && split == 0 && threadIdx.x == 0 && a.status;
     const int rows = sp.count * a.G, group0 = qb * kRowsPerGroup;
-    const int row0 = group0 + (kShares ? w * QT * 16 : 0);  // this wave's first row
+    // this wave's row tiles: every fourth of them where the waves divide the rows.  A
+    // wave skips a QT-th tile it lacks: 9 tiles are 3, 2, 2, 2 (105 us for 64 ragged
+    // trees of 33, and 109 as 3, 3, 3, 0), 5 are 2, 1, 1, 1 (115 and 124 us)
+    auto tile_row = [&](int t) { return group0 + (kShares ? t * kWavesPerBlock + w : t) * 16; };
+    const bool last = !kShares || QT == 1 || tile_row(QT - 1) < rows;
     if (!sp.ok || rows == 0) {
         if (split == 0) {  // a malformed request reads as zeros
             for (int i = threadIdx.x; i < kRowsPerGroup * D; i += kBlock) {
@@ -419,7 +423,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     u32x4 qr[kQInLds ? 1 : QT][kChunks];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        const int r = row0 + t * 16 + col;
+        const int r = tile_row(t) + col;
         const bool live = r < rows;
         const int n = live ? r / a.G : 0, g = live ? r % a.G : 0;
         sees[t] = __shfl(anc, n, kWave);
@@ -543,7 +547,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                 wait_loads<0>();
             asm volatile("s_barrier" ::: "memory");
             if (tile + R::kStages - 1 < t1) issue(tile + R::kStages - 1);
-            if (row0 >= rows) continue;  // a wave without rows only loads
+            if (tile_row(0) >= rows) continue;  // a wave without rows only loads
             stage = static_cast<uint32_t>((tile - t0) % R::kStages * R::kStageB);
             kv.read_k(ka, stage);
             if constexpr (E4M3) kv.read_scales(ring + stage + 64 * R::kRowB + w * 256 + kg * 16);
@@ -561,6 +565,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             const bf16x8 k0 = kv.k_slice(0, c), k1 = kv.k_slice(1, c);
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
+                if (kShares && t == QT - 1 && !last) continue;
                 const bf16x8 q = q_slice(t, c);
                 sc[t][0] = mfma16(k0, q, sc[t][0]);
                 sc[t][1] = mfma16(k1, q, sc[t][1]);
@@ -607,6 +612,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
+            if (kShares && t == QT - 1 && !last) continue;
             // weights relative to 2^ref.  The reference stays while no weight exceeds
             // 2^kSlack: a few exponents more cost fp32 sums and bf16 weights nothing
             float p[8];
@@ -648,13 +654,15 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             bf16x8 vt[kv.kWordVals];
             kv.transpose(i, vt);
 #pragma unroll
-            for (int e = 0; e < kv.kWordVals; ++e)
+            for (int t = 0; t < QT; ++t) {
+                if (kShares && t == QT - 1 && !last) continue;
 #pragma unroll
-                for (int t = 0; t < QT; ++t) {
+                for (int e = 0; e < kv.kWordVals; ++e) {
                     f32x4 &x = o[t][i * kv.kWordVals + e];
                     x = mfma16(vt[e], pf[t], x);
                     if constexpr (kTwoTerms) x = mfma16(vt[e], pl[t], x);
                 }
+            }
         }
         if (!kShares && more) kv.load_v(a, next, col, kg);
         if (odd) {
@@ -666,6 +674,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                                       (s & page_mask)) * D;
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
+                    if (kShares && t == QT - 1 && !last) continue;
                     float mine = 0.0f;
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
@@ -695,7 +704,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
         const int any = ballot(bad) != 0;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            const int r = row0 + t * 16 + col;
+            const int r = tile_row(t) + col;
             const float L = quad_sum(l[t]);
             if (r >= rows) continue;
             if (sp.active == 1) {
@@ -714,7 +723,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                     }
                 if (a.lse && kg == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(ref[t], L);
             } else {
-                const long long at = unit * kRowsPerGroup + (w * QT + t) * 16 + col;
+                const long long at = unit * kRowsPerGroup + (t * kWavesPerBlock + w) * 16 + col;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -756,7 +765,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
         __syncthreads();
         for (int i = threadIdx.x; i < 16 * (D / 4); i += kBlock) {
             const int rr = i / (D / 4), d = i % (D / 4) * 4;
-            const int r = row0 + t * 16 + rr;
+            const int r = tile_row(t) + rr;
             if (r >= rows) break;
             float M = sm[0][rr];
 #pragma unroll
