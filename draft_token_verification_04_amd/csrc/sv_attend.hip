@@ -44,7 +44,7 @@
 // Bounds and figures (MI355X, 32 query and 8 KV heads of 128): one token, 64
 // requests of 8192: 346 us, 6.2 TB/s of cache, bound by memory; lengths 64..8192:
 // 170 us, 5.5 TB/s, the rest the tail of the longest; e4m3: 5.3 TB/s, half the
-// bytes in flight per wave; 64 trees of 33: 105 us, bound by a tile's chain of
+// bytes in flight per wave; 64 trees of 33: 101 us, bound by a tile's chain of
 // LDS reads, products and exponentials with two waves per SIMD (registers).
 //
 // Masked slots: scores are replaced, never added to; value rows behind the
@@ -555,6 +555,10 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             find_rows(tile + 1, next);
         }
 
+        // kShared: while a wave has products to issue it goes before its SIMD's other
+        // wave, whose exponentials fill the gaps (64 ragged trees of 33: 101 us against
+        // 105, in e4m3 at equal lengths 153 and 157)
+        if constexpr (kShares) __builtin_amdgcn_s_setprio(1);
         // scores: slot s0 + 16 f + 4 kg + j of row col
         f32x4 sc[QT][2];
 #pragma unroll
@@ -608,6 +612,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             odd = ballot(odd) != 0;
         }
 
+        if constexpr (kShares) __builtin_amdgcn_s_setprio(0);
         bf16x8 pf[QT], pl[kTwoTerms ? QT : 1];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
@@ -648,6 +653,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                 pl[t] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
             }
         }
+        if constexpr (kShares) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < kv.kVWords; ++i) {
             if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
@@ -664,6 +670,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                 }
             }
         }
+        if constexpr (kShares) __builtin_amdgcn_s_setprio(0);
         if (!kShares && more) kv.load_v(a, next, col, kg);
         if (odd) {
             // the non-finite values, one by one, for the rows that see their token
