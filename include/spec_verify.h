@@ -427,8 +427,8 @@ sv_status spec_append_kv_paged(const void *q, const void *k, const void *v, long
  *   req_status [B] optional: 0; 1 a slot is outside the table (or base[b] < 0), or a
  *     page outside the cache; 2 the parent array is malformed.  The rows of a
  *     request with a non-zero status are 0, their lse -inf.
- * Weights enter the second product as two bf16 terms, or rounded to one where a KV
- * head has more than 32 rows; sums and references are fp32.
+ * Weights enter the second product as two bf16 terms, or rounded to one in some
+ * windows where a KV head has more than 32 rows; sums and references are fp32.
  * Scores (scale q.k) must lie within +-1e29; lower ones read as masked.
  * What a masked slot holds, infinities and NaN included, reaches no row.
  * Workspace: sv_attend_workspace_bytes (0 for invalid or unsupported sizes).
