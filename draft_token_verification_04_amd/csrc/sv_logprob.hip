@@ -139,10 +139,16 @@ __device__ __forceinline__ bool padding(const int32_t *__restrict__ tokens, long
 // Keeps a register's value from being derived again from an earlier one.
 __device__ __forceinline__ void opaque(u32x4 &x) { asm volatile("" : "+v"(x)); }
 
-// Sums of 2^d and 2^d d over a lane's vectors.  PLAIN forms d = x c - m c in one
-// step; it needs m c and every finite x c representable or far below m c, which
-// holds unless m itself is near the largest float.
-template <typename E, int U, bool PLAIN>
+// |m| c below which d is formed in one step, as fma(x, c, -fp32(m c)): half the
+// instructions of (x - m) c.  All of a segment's exponents are then off by the
+// rounding e of m c, at most 2^-11 here, which its sums take back by two terms of
+// the series of 2^e (the third: e^3 / 18 < 2^-37).  The rounding grows with |m c|: at
+// 2^24 it is half a step of the exponent itself, and a mask value of -1e10 would make
+// a segment's weights 2^328.  Logits within +-2^14 T / log2(e), 11000 T, are below.
+constexpr float kOneStep = 0x1p14f;
+
+// Sums of 2^d and 2^d d over a lane's vectors, d in one step or as (x - m) c.
+template <typename E, int U, bool ONE_STEP>
 __device__ __forceinline__ void lane_sums(u32x4 (&x)[U], float m, float c, float &s, float &t) {
     constexpr int P = E::kPerVec;
     const float R = m * c;
@@ -152,7 +158,7 @@ __device__ __forceinline__ void lane_sums(u32x4 (&x)[U], float m, float c, float
         unpack(make_uint4(x[u].x, x[u].y, x[u].z, x[u].w), v);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-            d[e] = PLAIN ? fmaf(v[e], c, -R) : (v[e] - m) * c;
+            d[e] = ONE_STEP ? fmaf(v[e], c, -R) : (v[e] - m) * c;
             v[e] = fast_exp2(d[e]);
             d[e] = fmaxf(d[e], -300.0f);  // 2^d d is 0 for a logit of -inf
         }
@@ -262,16 +268,16 @@ __global__ __launch_bounds__(kBlock, 4) void k_logprob(const typename E::storage
     double S = 0.0, Us = 0.0;
     if (m != ninf) {
         float s = 0.0f, t = 0.0f;
-        if (fabsf(m) * c < 0x1p120f)
+        const bool one_step = fabsf(m) * c < kOneStep;
+        if (one_step)
             lane_sums<E, U, true>(x, m, c, s, t);
         else
             lane_sums<E, U, false>(x, m, c, s, t);
         const double v = wave_sum_pair(static_cast<double>(s), static_cast<double>(t));
         S = v;
         Us = __shfl(v, 32, kWave);
-        if (fabsf(m) * c < 0x1p120f) {
-            // the one-step form is relative to fp32(m c): d is too small by e (|e| < 2^-16
-            // in any sane range), so S gains the factor 2^e = 1 + e ln 2 (1 + e ln 2 / 2)
+        if (one_step) {
+            // d is too small by e, so S gains the factor 2^e = 1 + e ln 2 (1 + e ln 2 / 2)
             const double e = static_cast<double>(m * c) - static_cast<double>(m) * static_cast<double>(c);
             const double f = 1.0 + e * kLn2d * (1.0 + 0.5 * e * kLn2d);
             Us = f * (Us + e * S);
