@@ -139,10 +139,10 @@ __device__ __forceinline__ bool padding(const int32_t *__restrict__ tokens, long
 // Keeps a register's value from being derived again from an earlier one.
 __device__ __forceinline__ void opaque(u32x4 &x) { asm volatile("" : "+v"(x)); }
 
-// |m| c below which d is formed in one step, as fma(x, c, -fp32(m c)): half the
-// instructions of (x - m) c.  All of a segment's exponents are then off by the
-// rounding e of m c, at most 2^-11 here, which its sums take back by two terms of
-// the series of 2^e (the third: e^3 / 18 < 2^-37).  The rounding grows with |m c|: at
+// |m| c below which d is formed in one step, as fma(x, c, -fp32(m c)), where
+// (x - m) c takes two instructions.  All of a segment's exponents are then off by
+// the rounding e of m c, at most 2^-11 here, which its sums take back by two terms
+// of the series of 2^e (the third: e^3 / 18 < 2^-37).  The rounding grows with |m c|: at
 // 2^24 it is half a step of the exponent itself, and a mask value of -1e10 would make
 // a segment's weights 2^328.  Logits within +-2^14 T / log2(e), 11000 T, are below.
 constexpr float kOneStep = 0x1p14f;
@@ -283,6 +283,17 @@ __global__ __launch_bounds__(kBlock, 4) void k_logprob(const typename E::storage
             Us = f * (Us + e * S);
             S *= f;
         }
+    } else {
+        // nothing but -inf, or NaN, which the maximum passes over and the sums must not
+        bool nan = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[P];
+            unpack(make_uint4(x[u].x, x[u].y, x[u].z, x[u].w), v);
+#pragma unroll
+            for (int e = 0; e < P; ++e) nan |= v[e] != v[e];
+        }
+        if (ballot(nan) != 0) S = __builtin_nan("");
     }
     if (lane == 0) parts[wave] = LogprobPart{S, Us, m, 0.0f};
 }
@@ -433,15 +444,18 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
     }
     // the sums, while the groups' logits are on their way
     double S = 0.0, Us = 0.0;
-    if (M != ninf) {
-        for (int s = threadIdx.x; s < segs; s += kBlock) {
-            if (s >= kBlock) mine = pp[s];
-            if (mine.m == ninf) continue;
-            // the factor in fp32: off by 2^-22 (1 + |g|) of a share 2^g of the sum
-            const double g = shifted(mine.m), f = fast_exp2(static_cast<float>(g));
-            S += mine.S * f;
-            Us += f * (mine.U + mine.S * g);
+    for (int s = threadIdx.x; s < segs; s += kBlock) {
+        if (s >= kBlock) mine = pp[s];
+        if (mine.m == ninf) {
+            S += mine.S;  // 0, or NaN where the segment holds one
+            continue;
         }
+        // the factor in fp32: off by 2^-22 (1 + |g|) of a share 2^g of the sum
+        const double g = shifted(mine.m), f = fast_exp2(static_cast<float>(g));
+        S += mine.S * f;
+        Us += f * (mine.U + mine.S * g);
+    }
+    {
         const double v = wave_sum_pair(S, Us);
         if (lane == 0) sS[w] = v;
         if (lane == 32) sU[w] = v;
@@ -479,7 +493,7 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
                     for (int e = 0; e < P; ++e) {
                         const int i = first + e;
                         const uint64_t key = argmax_key(v[e], i);
-                        list.push(key, from >= 0 && i >= 0 && i < V && key > list.bar, lane);
+                        list.push(key, from >= 0 && i >= 0 && i < V && v[e] == v[e] && key > list.bar, lane);
                     }
                     todo &= ballot(best > list.bar);
                 }
@@ -493,9 +507,11 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
     S = sS[0] + sS[1] + sS[2] + sS[3];
     Us = sU[0] + sU[1] + sU[2] + sU[3];
     const double L = log2(S);
+    const bool nan = S != S;  // the row holds a NaN, or +inf, whose 2^d is 2^(inf - inf)
+    auto log_prob = [&](float x) { return x == ninf ? ninf : static_cast<float>(kLn2d * (shifted(x) - L)); };
     if (lane == 0) {
-        if (logprob) logprob[row] = xt == ninf ? ninf : static_cast<float>(kLn2d * (shifted(xt) - L));
-        if (entropy) entropy[row] = M == ninf ? 0.0f : static_cast<float>(kLn2d * (L - Us / S));
+        if (logprob) logprob[row] = nan && in ? static_cast<float>(S) : log_prob(xt);
+        if (entropy) entropy[row] = M == ninf && !nan ? 0.0f : static_cast<float>(kLn2d * (L - Us / S));
         if (status) status[row] = tokens && !in ? 1 : 0;
     }
     if (k == 0) return;
@@ -508,7 +524,7 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
         const uint64_t key = lane < list.n ? list.buf[lane] : 0;
         const float x = key_value(key);
         top_ids[row * k + lane] = key ? argmax_key_index(key) : -1;
-        top_logprobs[row * k + lane] = key == 0 || x == ninf ? ninf : static_cast<float>(kLn2d * (shifted(x) - L));
+        top_logprobs[row * k + lane] = key == 0 ? ninf : (nan ? static_cast<float>(S) : log_prob(x));
     }
 }
 
