@@ -63,13 +63,39 @@ namespace {
 
 constexpr int kTile = 32;          // slots a wave takes per step
 constexpr float kSlack = 8.0f;     // weights may reach 2^kSlack before the reference moves
-// The reference of a row that has met no score (log2 units; a score so low, in
-// these units, would read as masked).  2^(kNoRef - any reference) is 0.
-constexpr float kNoRef = -1e30f;
 
-// Natural log of L 2^ref.
-__device__ __forceinline__ float log_sum(float ref, float L) {
-    return static_cast<float>((static_cast<double>(ref) + static_cast<double>(log2f(L))) * 0.6931471805599453);
+// A row's weights are 2^(s c) relative to 2^(m c), m its reference (a score q.k).
+// Where |m c| < kNear the exponent is one fma, s c - shift with shift = fp32(m c),
+// whose rounding (up to 2^-5) all of the row's weights and their sum share.  It grows
+// with |m c|, and from 2^31 on would overflow or lose every weight; there the exponent
+// is (s - m) c, and shift is kFar: the fma of any score that is not masked then lies
+// above kSlack, which leads to the step that knows m.  m itself waits in LDS (64 ragged
+// trees of 33: 94.9 -> 96.5 us a call; 32 chains in e4m3 44.0 -> 45.3, the others equal;
+// a branch of its own for near rows, which need not read m: 99 and 45).
+constexpr float kNear = 0x1p20f, kFar = -3e38f;
+// The reference of a row that has met no score.
+constexpr float kNoRef = -3.4028234663852886e38f;
+
+__device__ __forceinline__ float shift_of(float m, float c) {
+#pragma clang fp contract(off)
+    const float x = m * c;
+    return fabsf(x) < kNear ? x : kFar;
+}
+// The exponent of score s relative to reference m.
+__device__ __forceinline__ float relative(float s, float m, float shift, float c) {
+    return shift != kFar ? fmaf(s, c, -shift) : (s - m) * c;
+}
+// log2 of what turns weights relative to one reference into those of another.
+__device__ __forceinline__ float rebase(float m, float shift, float to, float to_shift, float c) {
+    if (shift == kFar) return relative(m, to, to_shift, c);
+    return to_shift == kFar ? fmaf(-to, c, shift) : shift - to_shift;
+}
+
+// Natural log of L 2^(m c).
+__device__ __forceinline__ float log_sum(float m, float L, float c) {
+    const float shift = shift_of(m, c);
+    const double x = shift != kFar ? static_cast<double>(shift) : static_cast<double>(m) * static_cast<double>(c);
+    return static_cast<float>((x + static_cast<double>(log2f(L))) * 0.6931471805599453);
 }
 
 __device__ __forceinline__ f32x4 mfma16(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
@@ -378,6 +404,8 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
         float o[kShares ? 1 : kWavesPerBlock][16][D + kPad];
         char ring[kShares ? Ring<D, E4M3>::kStages * Ring<D, E4M3>::kStageB : 16];
     } lds;
+    // the rows' reference scores; the walk itself needs only their shifts
+    __shared__ float refs[QT][kBlock];
     __shared__ float sm[kWavesPerBlock][16], sl[kWavesPerBlock][16];
     __shared__ int sbad;
     const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
@@ -450,10 +478,11 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     };
 
     f32x4 o[QT][kVals];
-    float ref[QT], l[QT];  // log2 of what the weights are relative to, and their sum
+    float shift[QT], l[QT];  // of the reference, and the weights' sum
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        ref[t] = kNoRef;
+        refs[t][threadIdx.x] = kNoRef;
+        shift[t] = shift_of(kNoRef, a.c);
         l[t] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVals; ++i) o[t][i] = f32x4{0, 0, 0, 0};
@@ -496,19 +525,23 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
     const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS char *)lds.ring));
     uint32_t ka[kv.kKVecs], va[4];
     auto issue = [&](int tile) {
+        long long next[2];
         find_rows(tile, next);
+        // opaque: as elements of `next`, picked by an index, they would pass through memory
+        long long row0 = next[0], row1 = next[1];
+        asm volatile("" : "+s"(row0), "+s"(row1));
         char *stage = lds.ring + (tile - t0) % R::kStages * R::kStageB;
 #pragma unroll
         for (int i = 0; i < R::kPerWave; ++i) {
             const int piece = i * kWavesPerBlock + w, of = piece % (R::kPieces / 2);
             const int r = of * (1024 / R::kRowB) + lane / R::kRowChunks;  // the row this lane loads from
             const char *from = static_cast<const char *>(piece < R::kPieces / 2 ? a.k_pages : a.v_pages) +
-                               next[of / (R::kPieces / 4)] * R::kRowB + (r & 15) * R::kRowB +
+                               (of < R::kPieces / 4 ? row0 : row1) * R::kRowB + (r & 15) * R::kRowB +
                                ((lane % R::kRowChunks) ^ R::swizzle(r)) * 16;
             __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from, (SV_LDS void *)(stage + piece * 1024), 16, 0, 0);
         }
         if constexpr (E4M3) {
-            const float *from = (lane < 32 ? a.k_scale : a.v_scale) + ((lane & 16) ? next[1] : next[0]) + col;
+            const float *from = (lane < 32 ? a.k_scale : a.v_scale) + ((lane & 16) ? row1 : row0) + col;
             __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from, (SV_LDS void *)(stage + 64 * R::kRowB + w * 256), 4, 0, 0);
         }
     };
@@ -618,23 +651,25 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
         for (int t = 0; t < QT; ++t) {
             if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
             if (kShares && t == QT - 1 && !last) continue;
-            // weights relative to 2^ref.  The reference stays while no weight exceeds
+            // weights relative to the reference, which stays while none exceeds
             // 2^kSlack: a few exponents more cost fp32 sums and bf16 weights nothing
             float p[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = fmaf(sc[t][e / 4][e % 4], a.c, -ref[t]);
+            for (int e = 0; e < 8; ++e) p[e] = fmaf(sc[t][e / 4][e % 4], a.c, -shift[t]);
             const float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
             if (ballot(top > kSlack) != 0) {
                 float most = sc[t][0][0];
 #pragma unroll
                 for (int e = 1; e < 8; ++e) most = fmaxf(most, sc[t][e / 4][e % 4]);
-                const float to = fmaxf(ref[t], quad_max(most) * a.c), f = fast_exp2(ref[t] - to);
+                const float from = refs[t][threadIdx.x], to = fmaxf(from, quad_max(most)), now = shift_of(to, a.c);
+                const float f = fast_exp2(rebase(from, shift[t], to, now, a.c));
                 l[t] *= f;
 #pragma unroll
                 for (int i = 0; i < kVals; ++i) o[t][i] *= f;
-                ref[t] = to;
+                refs[t][threadIdx.x] = to;
+                shift[t] = now;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = fmaf(sc[t][e / 4][e % 4], a.c, -to);
+                for (int e = 0; e < 8; ++e) p[e] = relative(sc[t][e / 4][e % 4], to, now, a.c);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[e] = fast_exp2(p[e]);
@@ -728,7 +763,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                                            pack_bf16(o[t][i + 2][j] * f, o[t][i + 3][j] * f));
                         *reinterpret_cast<uint2 *>(a.out + to * D + (kg * 4 + j) * kVals + i) = y;
                     }
-                if (a.lse && kg == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(ref[t], L);
+                if (a.lse && kg == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(refs[t][threadIdx.x], L, a.c);
             } else {
                 const long long at = unit * kRowsPerGroup + (t * kWavesPerBlock + w) * 16 + col;
 #pragma unroll
@@ -738,7 +773,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                         *reinterpret_cast<float4 *>(a.part_o + at * D + (kg * 4 + j) * kVals + i) =
                             make_float4(o[t][i][j], o[t][i + 1][j], o[t][i + 2][j], o[t][i + 3][j]);
                 if (kg == 0) {
-                    a.part_ml[at * 2] = ref[t];
+                    a.part_ml[at * 2] = refs[t][threadIdx.x];
                     a.part_ml[at * 2 + 1] = L;
                 }
             }
@@ -759,7 +794,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
         if (t > 0) __syncthreads();
         const float ll = quad_sum(l[t]);
         if (kg == 0) {
-            sm[w][col] = ref[t];
+            sm[w][col] = refs[t][threadIdx.x];
             sl[w][col] = ll;
         }
         // the lane's values: d = (4 kg + j) kVals + i
@@ -777,11 +812,12 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
             float M = sm[0][rr];
 #pragma unroll
             for (int v = 1; v < kWavesPerBlock; ++v) M = fmaxf(M, sm[v][rr]);
+            const float shift_M = shift_of(M, a.c);
             float L = 0.0f;
             float4 x = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int v = 0; v < kWavesPerBlock; ++v) {
-                const float f = fast_exp2(sm[v][rr] - M);
+                const float m = sm[v][rr], f = fast_exp2(rebase(m, shift_of(m, a.c), M, shift_M, a.c));
                 L += sl[v][rr] * f;
                 const float4 y = *reinterpret_cast<const float4 *>(&lds.o[v][rr][d]);
                 x.x += y.x * f;
@@ -796,7 +832,7 @@ __global__ __launch_bounds__(kBlock, 2) void k_attend(AttendArgs a) {
                 uint2 y = make_uint2(0, 0);
                 if (!none) y = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
                 *reinterpret_cast<uint2 *>(a.out + to * D + d) = y;
-                if (a.lse && d == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(M, L);
+                if (a.lse && d == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(M, L, a.c);
             } else {
                 const long long at = unit * kRowsPerGroup + t * 16 + rr;
                 *reinterpret_cast<float4 *>(a.part_o + at * D + d) = x;
@@ -840,6 +876,7 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int group_
     }
     bad = ballot(bad) != 0;
     M = wave_max(M);
+    const float shift_M = shift_of(M, a.c);
     float L = 0.0f, x[kPer] = {};
     for (int s0 = wj; s0 < sp.active; s0 += kAhead * JW) {
         float y[kAhead][kPer], ms[kAhead], ls[kAhead];
@@ -854,7 +891,7 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int group_
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (s0 + i * JW >= sp.active) continue;
-            const float f = fast_exp2(ms[i] - M);
+            const float f = fast_exp2(rebase(ms[i], shift_of(ms[i], a.c), M, shift_M, a.c));
             L += ls[i] * f;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) x[e] += y[i][e] * f;
@@ -885,7 +922,7 @@ __global__ __launch_bounds__(kBlock) void k_attend_join(AttendArgs a, int group_
             *reinterpret_cast<unsigned *>(out + e) = none ? 0 : pack_bf16(x[e] * f, x[e + 1] * f);
     }
     if (lane == 0) {
-        if (a.lse) a.lse[to] = none ? ninf : log_sum(M, L);
+        if (a.lse) a.lse[to] = none ? ninf : log_sum(M, L, a.c);
         if (a.status && h == 0 && r == 0) a.status[b] = bad ? 1 : 0;
     }
 }

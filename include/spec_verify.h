@@ -429,7 +429,8 @@ sv_status spec_append_kv_paged(const void *q, const void *k, const void *v, long
  *     request with a non-zero status are 0, their lse -inf.
  * Weights enter the second product as two bf16 terms, or rounded to one in some
  * windows where a KV head has more than 32 rows; sums and references are fp32.
- * Scores (scale q.k) must lie within +-1e29; lower ones read as masked.
+ * Scores (scale q.k) must lie within +-1e29 and q.k within fp32; the weights are formed
+ * from differences of scores, of any size.
  * What a masked slot holds, infinities and NaN included, reaches no row.
  * Workspace: sv_attend_workspace_bytes (0 for invalid or unsupported sizes).
  */
