@@ -694,8 +694,7 @@ bool attend_sizes_ok(int B, int N, int H, int kv_heads, int head_dim, int P, int
     if (N > SV_MAX_WINDOW || H > 65536 || static_cast<double>(B) * N * H > 2.0e9) return false;
     if (B == 0) return true;
     const AttendPlan p = attend_plan(B, N, H, kv_heads, head_dim, P, page_size);
-    // workgroups of the grid, rounded up to whole octets
-    return (static_cast<double>(p.S) * B * kv_heads + 8.0) * p.QB < 2147483647.0;
+    return attend_groups(B, kv_heads, p) <= kMaxGroups && attend_join_groups(B, N, H, p) <= kMaxGroups;
 }
 
 }  // namespace
@@ -717,7 +716,7 @@ sv_status spec_append_kv_paged(const void *q, const void *k, const void *v, long
         if (rot < 1 || rot > D || max_pos < 1) return SV_ERR_INVALID_ARG;
         if (rot % 16 != 0) return SV_ERR_UNSUPPORTED;
     }
-    if (static_cast<long long>(B) * N > 0x7fffffffLL || static_cast<long long>(H) + 2LL * cache.kv_heads > 65536)
+    if (static_cast<long long>(B) * N > kMaxGroups || static_cast<long long>(H) + 2LL * cache.kv_heads > 65536)
         return SV_ERR_UNSUPPORTED;
     if (B == 0) return SV_OK;
     if (!q || !k || !v || !base || !page_table || !q_out || (rope && !positions)) return SV_ERR_INVALID_ARG;
@@ -849,7 +848,9 @@ sv_status spec_commit_tree_kv_paged(void *pages, float *scales, int G, int num_p
         row_bytes > 1024 || N > SV_MAX_TREE_NODES || kv_heads > 32768 || static_cast<long long>(P) * page_size > kMaxSlots ||
         static_cast<double>(G) * B * kv_heads > 2.0e9)
         return SV_ERR_UNSUPPORTED;
-    if (static_cast<double>(G) * num_pages * kv_heads * page_size * row_bytes >= 9.0e18) return SV_ERR_UNSUPPORTED;
+    if (static_cast<double>(G) * num_pages * kv_heads * page_size * row_bytes >= 9.0e18 ||
+        commit_paged_groups(G, B, kv_heads) > kMaxGroups)
+        return SV_ERR_UNSUPPORTED;
     if (B == 0) return SV_OK;
     if (!pages || !page_table || !tree_base || !commit_base || !accept_len || !path_nodes) return SV_ERR_INVALID_ARG;
     if (!aligned16(pages)) return SV_ERR_INVALID_ARG;
@@ -876,12 +877,17 @@ LogprobWs logprob_ws_layout(int R, int V, sv_dtype dt, int k) {
     w.total = w.group_maxima + (k > 0 ? align_up(n * 64 * sizeof(float)) : 0);
     return w;
 }
+// a workgroup per row, and a wave per segment
+bool logprob_sizes_ok(int R, int V, sv_dtype dt) {
+    return sizes_ok(R, 1, V) && R <= kMaxGroups &&
+           static_cast<long long>(R) * logprob_segs(R, V, dt) <= kMaxGroups * kWavesPerBlock;
+}
 }  // namespace
 
 extern "C" {
 
 size_t sv_token_logprobs_workspace_bytes(int R, int V, sv_dtype dt, int top_k) {
-    if (R < 1 || !valid_dtype(dt) || top_k < 0 || top_k > SV_MAX_TOP || top_k > V || !sizes_ok(R, 1, V)) return 0;
+    if (R < 1 || !valid_dtype(dt) || top_k < 0 || top_k > SV_MAX_TOP || top_k > V || !logprob_sizes_ok(R, V, dt)) return 0;
     return logprob_ws_layout(R, V, dt, top_k).total;
 }
 
@@ -892,7 +898,7 @@ sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, 
     if (!valid_dtype(dt)) return SV_ERR_UNSUPPORTED;
     if (R < 0 || V < 1 || top_k < 0 || top_k > V || !(temperature > 0.0f) || !isfinite(temperature))
         return SV_ERR_INVALID_ARG;
-    if (top_k > SV_MAX_TOP || !sizes_ok(R, 1, V)) return SV_ERR_UNSUPPORTED;
+    if (top_k > SV_MAX_TOP || !logprob_sizes_ok(R, V, dt)) return SV_ERR_UNSUPPORTED;
     if (R == 0) return SV_OK;
     if (!logits || !workspace || !aligned256(workspace) || (logprob && !tokens) ||
         (top_k > 0 && (!top_ids || !top_logprobs)))
@@ -900,7 +906,7 @@ sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, 
     if (reinterpret_cast<uintptr_t>(logits) % (dt == SV_BF16 ? 2 : 4) != 0) return SV_ERR_INVALID_ARG;
     const double c = 1.4426950408889634073599246810018921 / static_cast<double>(temperature);
     const int segs = logprob_segs(R, V, dt);
-    if (!(c < 0x1p127) || static_cast<double>(R) * segs > 8.0e9) return SV_ERR_UNSUPPORTED;
+    if (!(c < 0x1p127)) return SV_ERR_UNSUPPORTED;
     const LogprobWs L = logprob_ws_layout(R, V, dt, top_k);
     if (workspace_bytes < L.total) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);

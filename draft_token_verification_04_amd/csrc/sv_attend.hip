@@ -1004,9 +1004,19 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     return p;
 }
 
+long long attend_groups(int B, int Hkv, const AttendPlan &p) {
+    return (static_cast<long long>(p.S) * B * Hkv + 7) / 8 * 8 * p.QB;
+}
+// few rows, of many splits each as a rule: four waves a row (160 rows of 128
+// splits 9 us against 17); many: a wave a row (8192 rows of 2 splits 7 against 19)
+static constexpr long long kFewRows = 2048;
+long long attend_join_groups(int B, int N, int H, const AttendPlan &p) {
+    const long long rows = static_cast<long long>(B) * N * H;
+    return p.S <= 1 ? 0 : (rows <= kFewRows ? rows : (rows + kWavesPerBlock - 1) / kWavesPerBlock);
+}
+
 hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan &p, hipStream_t s) {
-    const long long rest = static_cast<long long>(a.S) * a.B * a.Hkv;
-    const dim3 grid(static_cast<unsigned>((rest + 7) / 8 * 8 * a.QB));
+    const dim3 grid(static_cast<unsigned>(attend_groups(a.B, a.Hkv, p)));
     const int QT = p.QT;
     const bool sh = p.shares;
     if (D == 64) return e4m3 ? launch_qt<64, true>(a, QT, sh, grid, s) : launch_qt<64, false>(a, QT, sh, grid, s);
@@ -1016,21 +1026,18 @@ hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan
 
 namespace {
 template <int D>
-hipError_t launch_join(const AttendArgs &a, int group_rows, hipStream_t s) {
-    const long long rows = static_cast<long long>(a.B) * a.Hkv * a.N * a.G;
-    // few rows, of many splits each as a rule: four waves a row (160 rows of 128
-    // splits 9 us against 17); many: a wave a row (8192 rows of 2 splits 7 against 19)
-    if (rows <= 2048)
-        return launch_kernel(k_attend_join<D, 4>, dim3(static_cast<unsigned>(rows)), dim3(kBlock), 0, s, a, group_rows);
-    return launch_kernel(k_attend_join<D, 1>, dim3(static_cast<unsigned>((rows + kWavesPerBlock - 1) / kWavesPerBlock)),
-                         dim3(kBlock), 0, s, a, group_rows);
+hipError_t launch_join(const AttendArgs &a, const AttendPlan &p, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(attend_join_groups(a.B, a.N, a.H, p)));
+    if (static_cast<long long>(a.B) * a.N * a.H <= kFewRows)
+        return launch_kernel(k_attend_join<D, 4>, grid, dim3(kBlock), 0, s, a, p.group_rows);
+    return launch_kernel(k_attend_join<D, 1>, grid, dim3(kBlock), 0, s, a, p.group_rows);
 }
 }  // namespace
 
 hipError_t launch_attend_join(const AttendArgs &a, int D, const AttendPlan &p, hipStream_t s) {
-    if (D == 64) return launch_join<64>(a, p.group_rows, s);
-    if (D == 128) return launch_join<128>(a, p.group_rows, s);
-    return launch_join<256>(a, p.group_rows, s);
+    if (D == 64) return launch_join<64>(a, p, s);
+    if (D == 128) return launch_join<128>(a, p, s);
+    return launch_join<256>(a, p, s);
 }
 
 }  // namespace sv

@@ -149,15 +149,24 @@ __global__ __launch_bounds__(kBlock) void k_commit_paged(
 
 }  // namespace
 
+static int units_per_wave(int G, int B, int Hkv) {
+    const long long units = static_cast<long long>(G) * Hkv;
+    return static_cast<int>(std::min<long long>(64, std::max<long long>(1, (units * B + kCommitWaves - 1) / kCommitWaves)));
+}
+
+long long commit_paged_groups(int G, int B, int Hkv) {
+    const long long per = units_per_wave(G, B, Hkv), runs = (static_cast<long long>(G) * Hkv + per - 1) / per;
+    return (B * runs + kWavesPerBlock - 1) / kWavesPerBlock;
+}
+
 hipError_t launch_commit_paged(void *pages, float *scales, int G, int B, int Hkv, int num_pages, int page_shift,
                                int vecs, const int32_t *page_table, int P, const int32_t *tree_base,
                                const int32_t *commit_base, const int32_t *accept_len, const int32_t *path_nodes,
                                int N, int32_t *status, hipStream_t s) {
-    const long long units = static_cast<long long>(G) * Hkv;
-    const int per = static_cast<int>(std::min<long long>(64, std::max<long long>(1, (units * B + kCommitWaves - 1) / kCommitWaves)));
-    const int runs = static_cast<int>((units + per - 1) / per);
-    const long long blocks = (static_cast<long long>(B) * runs + kWavesPerBlock - 1) / kWavesPerBlock;
-    return launch_kernel(k_commit_paged, dim3(static_cast<unsigned>(blocks)), dim3(kBlock), 0, s,
+    const int per = units_per_wave(G, B, Hkv);
+    const int runs = static_cast<int>((static_cast<long long>(G) * Hkv + per - 1) / per);
+    const unsigned groups = static_cast<unsigned>(commit_paged_groups(G, B, Hkv));
+    return launch_kernel(k_commit_paged, dim3(groups), dim3(kBlock), 0, s,
                          static_cast<u32x4 *>(pages), scales, G, B, Hkv, num_pages, page_shift,
                          __builtin_ctz(static_cast<unsigned>(vecs)), per, runs, page_table, P, tree_base, commit_base,
                          accept_len, path_nodes, N, status);

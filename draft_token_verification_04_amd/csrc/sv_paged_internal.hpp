@@ -11,6 +11,9 @@ namespace sv {
 // and its inverse are then normal floats.
 constexpr float kMinAmax = 448.0f * 0x1p-126f;
 
+// Most workgroups of a launch along x: fewer than 2^32 work items.
+constexpr long long kMaxGroups = (1LL << 32) / 256 - 1;
+
 struct AppendArgs {
     const uint16_t *q, *k, *v;              // bf16 rows of token t at t * stride
     long long q_stride, k_stride, v_stride;
@@ -51,6 +54,7 @@ hipError_t launch_logprob_merge(const LogprobArgs &a, sv_dtype dt, hipStream_t s
 // Moves the accepted path's rows inside the pages: G arrays of pages
 // [num_pages][Hkv][page_size] rows of `vecs` (a power of two) 16-byte vectors,
 // and as many of one float per row (scales, may be null).
+long long commit_paged_groups(int G, int B, int Hkv);  // workgroups of the launch
 hipError_t launch_commit_paged(void *pages, float *scales, int G, int B, int Hkv, int num_pages, int page_shift,
                                int vecs, const int32_t *page_table, int P, const int32_t *tree_base,
                                const int32_t *commit_base, const int32_t *accept_len, const int32_t *path_nodes,
@@ -82,5 +86,8 @@ struct AttendPlan {
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size);
 hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan &p, hipStream_t s);
 hipError_t launch_attend_join(const AttendArgs &a, int D, const AttendPlan &p, hipStream_t s);
+// Workgroups of the two launches (the join's 0 where nothing is split).
+long long attend_groups(int B, int Hkv, const AttendPlan &p);
+long long attend_join_groups(int B, int N, int H, const AttendPlan &p);
 
 }  // namespace sv

@@ -373,6 +373,12 @@ typedef struct {
 #define SV_MAX_WINDOW 64
 /* Most alternatives per row spec_token_logprobs returns. */
 #define SV_MAX_TOP 32
+/*
+ * The four entry points below return SV_ERR_UNSUPPORTED (and the workspace queries 0)
+ * for sizes whose launch would exceed 2^24 - 1 workgroups of 256: an append has one
+ * for each of its B N tokens, log probabilities one for each row and one for every
+ * four segments of a row, an attention at least one for each request and KV head.
+ */
 
 /*
  * Writes a window's keys and values into a paged cache, with the per-head norms
