@@ -607,7 +607,9 @@ class PagedKV:
     k_pages and v_pages [num_pages, kv_heads, page_size, head_dim], contiguous, bfloat16
     or float8_e4m3fn; the latter with k_scales and v_scales [num_pages, kv_heads,
     page_size] float32.  page_size a power of two in [16, 1024], head_dim 64, 128
-    or 256.  The arrays may be slices of one allocation (``kv[layer, 0]``)."""
+    or 256.  The arrays may be slices of one allocation (``kv[layer, 0]``).  A PagedKV
+    is fixed once made, and its arrays must keep their storage (no ``resize_``, no
+    ``set_``): other arrays take another PagedKV."""
 
     def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
         import torch
@@ -635,6 +637,12 @@ class PagedKV:
                                  None if k_scales is None else k_scales.data_ptr(),
                                  None if v_scales is None else v_scales.data_ptr(), dt, self.num_pages,
                                  self.kv_heads, self.page_size, self.head_dim)
+
+    def __setattr__(self, name, value):
+        # an array put in another's place would leave calls at the old one's address
+        if "_c" in self.__dict__:
+            raise AttributeError(f"PagedKV.{name} is fixed; make another PagedKV")
+        super().__setattr__(name, value)
 
 
 def _window_rows(torch, t, name, heads, head_dim, dev, lead=None):
