@@ -694,7 +694,7 @@ bool attend_sizes_ok(int B, int N, int H, int kv_heads, int head_dim, int P, int
     if (N > SV_MAX_WINDOW || H > 65536 || static_cast<double>(B) * N * H > 2.0e9) return false;
     if (B == 0) return true;
     const AttendPlan p = attend_plan(B, N, H, kv_heads, head_dim, P, page_size);
-    return attend_groups(B, kv_heads, p) <= kMaxGroups && attend_join_groups(B, N, H, p) <= kMaxGroups;
+    return attend_groups(B, kv_heads, p) <= kMaxGroups;  // what is split has far fewer rows to join
 }
 
 }  // namespace

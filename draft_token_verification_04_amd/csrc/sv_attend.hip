@@ -974,8 +974,14 @@ hipError_t launch_qt(const AttendArgs &a, int QT, bool shares, dim3 grid, hipStr
 // so and 70 otherwise (e4m3 36 and 43), where all are 4096 long 102 and 93.  With
 // kTargetGroups pairs or more the join takes back what it gains (64 chains of 8
 // over lengths up to 2048: 57 + 9 against 69, all 2048 long 99 + 11 against 91).
+//
+// The splits are counted from the table's width, and a request is cut into as many of
+// them as have a least run.  A table much wider than its requests therefore cuts them
+// finer than the runs above and takes workspace for splits that stay unused, in all
+// at most kMaxPartials: 256 trees of 64 over tables of 2^20 slots would ask for 618 GB.
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size) {
     constexpr int kTargetGroups = 512, kRun = 8, kFineRun = 6, kSharedRun = 96;
+    constexpr long long kMaxPartials = 512LL << 20;
     AttendPlan p;
     const int rows = N * (H / Hkv), tiles = (rows + 15) / 16;
     p.shares = D <= 128 && tiles > 3;
@@ -993,7 +999,8 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
     long long want = std::max((kTargetGroups + groups - 1) / groups, (all + run - 1) / run);
     if (groups * want < 4 * kTargetGroups)  // whole rounds of the card: a part of one takes as long
         want = std::max(want, (groups * want + kTargetGroups - 1) / kTargetGroups * kTargetGroups / groups);
-    p.S = static_cast<int>(std::max(1LL, std::min({want, cap, 1024LL})));
+    const long long split_bytes = groups * p.group_rows * (D + 2) * 4;  // partials of one split of everything
+    p.S = static_cast<int>(std::max(1LL, std::min({want, cap, 1024LL, kMaxPartials / split_bytes})));
     p.falling = groups * p.S >= (fine ? 2 : 4) * kTargetGroups;
     const size_t units = static_cast<size_t>(groups) * p.S, n = units * p.group_rows;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
@@ -1007,13 +1014,6 @@ AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size
 long long attend_groups(int B, int Hkv, const AttendPlan &p) {
     return (static_cast<long long>(p.S) * B * Hkv + 7) / 8 * 8 * p.QB;
 }
-// few rows, of many splits each as a rule: four waves a row (160 rows of 128
-// splits 9 us against 17); many: a wave a row (8192 rows of 2 splits 7 against 19)
-static constexpr long long kFewRows = 2048;
-long long attend_join_groups(int B, int N, int H, const AttendPlan &p) {
-    const long long rows = static_cast<long long>(B) * N * H;
-    return p.S <= 1 ? 0 : (rows <= kFewRows ? rows : (rows + kWavesPerBlock - 1) / kWavesPerBlock);
-}
 
 hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan &p, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(attend_groups(a.B, a.Hkv, p)));
@@ -1026,18 +1026,21 @@ hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan
 
 namespace {
 template <int D>
-hipError_t launch_join(const AttendArgs &a, const AttendPlan &p, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(attend_join_groups(a.B, a.N, a.H, p)));
-    if (static_cast<long long>(a.B) * a.N * a.H <= kFewRows)
-        return launch_kernel(k_attend_join<D, 4>, grid, dim3(kBlock), 0, s, a, p.group_rows);
-    return launch_kernel(k_attend_join<D, 1>, grid, dim3(kBlock), 0, s, a, p.group_rows);
+hipError_t launch_join(const AttendArgs &a, int group_rows, hipStream_t s) {
+    const long long rows = static_cast<long long>(a.B) * a.Hkv * a.N * a.G;
+    // few rows, of many splits each as a rule: four waves a row (160 rows of 128
+    // splits 9 us against 17); many: a wave a row (8192 rows of 2 splits 7 against 19)
+    if (rows <= 2048)
+        return launch_kernel(k_attend_join<D, 4>, dim3(static_cast<unsigned>(rows)), dim3(kBlock), 0, s, a, group_rows);
+    return launch_kernel(k_attend_join<D, 1>, dim3(static_cast<unsigned>((rows + kWavesPerBlock - 1) / kWavesPerBlock)),
+                         dim3(kBlock), 0, s, a, group_rows);
 }
 }  // namespace
 
 hipError_t launch_attend_join(const AttendArgs &a, int D, const AttendPlan &p, hipStream_t s) {
-    if (D == 64) return launch_join<64>(a, p, s);
-    if (D == 128) return launch_join<128>(a, p, s);
-    return launch_join<256>(a, p, s);
+    if (D == 64) return launch_join<64>(a, p.group_rows, s);
+    if (D == 128) return launch_join<128>(a, p.group_rows, s);
+    return launch_join<256>(a, p.group_rows, s);
 }
 
 }  // namespace sv

@@ -86,8 +86,6 @@ struct AttendPlan {
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size);
 hipError_t launch_attend(const AttendArgs &a, int D, bool e4m3, const AttendPlan &p, hipStream_t s);
 hipError_t launch_attend_join(const AttendArgs &a, int D, const AttendPlan &p, hipStream_t s);
-// Workgroups of the two launches (the join's 0 where nothing is split).
-long long attend_groups(int B, int Hkv, const AttendPlan &p);
-long long attend_join_groups(int B, int N, int H, const AttendPlan &p);
+long long attend_groups(int B, int Hkv, const AttendPlan &p);  // workgroups of the first launch
 
 }  // namespace sv

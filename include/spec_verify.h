@@ -438,7 +438,8 @@ sv_status spec_append_kv_paged(const void *q, const void *k, const void *v, long
  * Scores (scale q.k) must lie within +-1e29 and q.k within fp32; the weights are formed
  * from differences of scores, of any size.
  * What a masked slot holds, infinities and NaN included, reaches no row.
- * Workspace: sv_attend_workspace_bytes (0 for invalid or unsupported sizes).
+ * Workspace: sv_attend_workspace_bytes (0 for invalid or unsupported sizes).  It grows
+ * with the table's width (P * page_size), which decides the splits, to about 512 MB.
  */
 size_t sv_attend_workspace_bytes(int B, int N, int H, int kv_heads, int head_dim, int P, int page_size);
 
