@@ -274,15 +274,15 @@ __global__ __launch_bounds__(kBlock, 4) void k_logprob(const typename E::storage
         else
             lane_sums<E, U, false>(x, m, c, s, t);
         const double v = wave_sum_pair(static_cast<double>(s), static_cast<double>(t));
-        S = v;
-        Us = __shfl(v, 32, kWave);
-        if (one_step) {
-            // d is too small by e, so S gains the factor 2^e = 1 + e ln 2 (1 + e ln 2 / 2)
-            const double e = static_cast<double>(m * c) - static_cast<double>(m) * static_cast<double>(c);
-            const double f = 1.0 + e * kLn2d * (1.0 + 0.5 * e * kLn2d);
-            Us = f * (Us + e * S);
-            S *= f;
-        }
+        // The maximum's own term, 2^0 and 0, is put in exactly: S is then at least 1, no
+        // probability exceeds it, and a lone token has logprob 0.  In one step every d
+        // is too small by e = -d0, so the other terms gain the factor
+        // 2^e = 1 + e ln 2 (1 + e ln 2 / 2)
+        const float R = m * c, d0 = one_step ? fmaf(m, c, -R) : 0.0f, own = fast_exp2(d0), own_d = own * d0;
+        const double y = -static_cast<double>(d0) * kLn2d, f = 1.0 + y * (1.0 + 0.5 * y);
+        const double rest = v - own;
+        S = 1.0 + f * rest;
+        Us = f * (__shfl(v, 32, kWave) - own_d - d0 * rest);
     } else {
         // nothing but -inf, or NaN, which the maximum passes over and the sums must not
         bool nan = false;
@@ -511,7 +511,8 @@ __global__ __launch_bounds__(kBlock) void k_logprob_merge(
     auto log_prob = [&](float x) { return x == ninf ? ninf : static_cast<float>(kLn2d * (shifted(x) - L)); };
     if (lane == 0) {
         if (logprob) logprob[row] = nan && in ? static_cast<float>(S) : log_prob(xt);
-        if (entropy) entropy[row] = M == ninf && !nan ? 0.0f : static_cast<float>(kLn2d * (L - Us / S));
+        const double h = L - Us / S;  // below 0 only by rounding
+        if (entropy) entropy[row] = (M == ninf && !nan) || h < 0.0 ? 0.0f : static_cast<float>(kLn2d * h);
         if (status) status[row] = tokens && !in ? 1 : 0;
     }
     if (k == 0) return;
