@@ -830,7 +830,7 @@ def spec_token_logprobs(logits, tokens=None, *, temperature=1.0, top_k=0, entrop
     or f32, contiguous), tokens [R] int32 (a row whose token is -1 is not read).
     Returns ``logprob`` [R] (with tokens), ``entropy`` [R] in nats, ``top_ids`` and
     ``top_logprobs`` [R, top_k] (top_k <= 32, by falling probability, ties to the
-    lowest id) and ``status`` [R]."""
+    lowest id) and ``status`` [R].  A row that holds NaN or +inf returns NaN."""
     torch = _torch()
     lib = load_library()
     _check(logits, "logits", 2)

@@ -173,9 +173,12 @@ hipError_t launch_d(const AppendArgs &a, bool e4m3, dim3 grid, hipStream_t s) {
 
 }  // namespace
 
-// Tokens from which a workgroup takes all of a token's rows, in passes, instead
-// of one pass's: lookups and angles are then read once per token.  8191 tokens of
-// 48 rows: 46 us against 61; 2112 (most of them padding): 11.4 against 10.8.
+// Tokens (padding among them) from which a workgroup takes all of a token's rows, in
+// passes, instead of one pass's: lookups and angles are then read once per token.  In
+// passes against not, 48 rows of 128 a token, bf16: 256 tokens 5.3 and 4.2 us, 1024
+// 7.5 and 8.2, 2112 13.0 and 14.3, 4096 18.9 and 24.1, 8191 33.9 and 46.1 (e4m3 36.9
+// and 49.6); 64 windows of up to 33, half of it padding, 9.9 both.  The two cross
+// below 1000 tokens; from 4096 on passes gain a fifth and more.
 constexpr int kWideTokens = 4096;
 
 hipError_t launch_append(const AppendArgs &a, int D, bool e4m3, int tokens, hipStream_t s) {

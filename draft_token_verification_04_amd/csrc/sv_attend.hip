@@ -24,10 +24,11 @@
 //                  serves 8 MFMAs, MFMA i holding values d = 8 m + i.
 // The weights enter the second product as two bf16 terms, the rounded weight and
 // the rounded rest (2^-16 relative): up to two row tiles per wave the products
-// that this adds are hidden behind the cache's bytes.  With three (windows of 33
-// rows per KV head and more), where they are not and the registers are full, it
-// takes the first term alone: at most 2^-8 relative for each weight, independent,
-// averaged over the slots.  l sums the weights unrounded, and every accumulator,
+// that this adds are hidden behind the cache's bytes.  With three (33 to 48 rows per
+// KV head where the slots are divided, nine to twelve row tiles of a workgroup where
+// the rows are), where they are not and the registers are full, it takes the first
+// term alone: at most 2^-8 relative for each weight, independent, averaged over the
+// slots.  l sums the weights unrounded, and every accumulator,
 // reference and sum is fp32.  An e4m3 cache is widened to bf16 in
 // registers (exact); its per-row scales multiply the scores and the weights.
 //
@@ -42,10 +43,13 @@
 // device, so a captured graph replays with other lengths.
 //
 // Bounds and figures (MI355X, 32 query and 8 KV heads of 128): one token, 64
-// requests of 8192: 346 us, 6.2 TB/s of cache, bound by memory; lengths 64..8192:
-// 170 us, 5.5 TB/s, the rest the tail of the longest; e4m3: 5.3 TB/s, half the
-// bytes in flight per wave; 64 trees of 33: 101 us, bound by a tile's chain of
-// LDS reads, products and exponentials with two waves per SIMD (registers).
+// requests of 8192: 353 us, 6.1 TB/s of cache, bound by memory; lengths up to 8192:
+// 166 us, 5.6 TB/s, the rest the tail of the longest; e4m3: 208 and 103 us, 5.3 and
+// 4.7 TB/s, half the bytes in flight per wave; 64 trees of 33 over up to 2048: 97 us,
+// all over 2048 130 us (541 TFLOP/s), in e4m3 118 and 141, bound by a tile's chain of
+// LDS reads, products and exponentials with two waves per SIMD (registers).  Heads
+// of 256 never share: 64 trees of 33, 8 query heads to one KV head, take 131 + 12 us
+// where the same bytes as 16 to 2 heads of 128 take 88 + 10.
 //
 // Masked slots: scores are replaced, never added to; value rows behind the
 // last token are zeroed; and a non-finite value of a window token is left to
@@ -977,8 +981,10 @@ hipError_t launch_qt(const AttendArgs &a, int QT, bool shares, dim3 grid, hipStr
 //
 // The splits are counted from the table's width, and a request is cut into as many of
 // them as have a least run.  A table much wider than its requests therefore cuts them
-// finer than the runs above and takes workspace for splits that stay unused, in all
-// at most kMaxPartials: 256 trees of 64 over tables of 2^20 slots would ask for 618 GB.
+// finer than the runs above (tables of 131072 slots: one token of 64 requests up to
+// 8192 245 us against 169, 32 e4m3 chains 59 against 36, 64 trees 97 + 19 against 97)
+// and takes workspace for splits that stay unused, in all at most kMaxPartials: 256
+// trees of 64 over tables of 2^20 slots would ask for 618 GB.
 AttendPlan attend_plan(int B, int N, int H, int Hkv, int D, int P, int page_size) {
     constexpr int kTargetGroups = 512, kRun = 8, kFineRun = 6, kSharedRun = 96;
     constexpr long long kMaxPartials = 512LL << 20;

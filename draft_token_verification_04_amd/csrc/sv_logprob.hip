@@ -16,9 +16,10 @@
 // Bound by the read of the logits; the exponentials (one per logit, at a
 // quarter of the rate of other instructions) come close to it, so the first
 // pass keeps to ten instructions per logit and selects nothing.  Measured at
-// 2048 rows of 151936 bf16 logits with 20 alternatives: 106 us (5.9 TB/s) and
-// 16 us; selecting the segment's 20 best in the first pass took 281 us and
-// 10 us, and a lane's own (strided) logits as the groups 106 us and 30 us.
+// 2048 rows of 151936 bf16 logits with 20 alternatives: 107 to 117 us (5.9 to 5.3
+// TB/s) and 14 to 16 us, at any temperature; selecting the segment's 20 best in the
+// first pass took 281 us and 10 us, and a lane's own (strided) logits as the groups
+// 106 us and 30 us.
 //
 // The k best: the k-th largest of 64 column maxima (a column: group l of every
 // segment) is a value that at least k logits reach.  Only groups whose maximum

@@ -402,7 +402,8 @@ typedef struct {
  *   token_status [B][N] optional: 0; 1 the slot is outside the table, or its
  *     page outside the cache; 2 the position is outside [0, max_pos).  A token
  *     with a non-zero status, or behind counts, writes nothing.
- * Everything is computed in fp32 and rounded once, to nearest even.  An e4m3
+ * Everything is computed in fp32 and rounded once, to nearest even (x^2 included: with
+ * the norm, |x| up to 1e18).  An e4m3
  * row is stored as round(y * (448 / a)) with scale a / 448, a = max |y| (a row
  * of zeros: scale 0).  A row that holds an infinity or NaN is stored so that it
  * reads back as NaN where it was not finite.
@@ -555,7 +556,7 @@ typedef enum {
     SV_K_ATTEND = 19,       /* attention of a window over a paged cache */
     SV_K_ATTEND_JOIN = 20,  /* its splits joined */
     SV_K_COMMIT_PAGED = 21, /* rows of accepted tree paths moved inside a paged cache */
-    SV_K_LOGPROB = 22,      /* row statistics and best tokens per segment */
+    SV_K_LOGPROB = 22,      /* row statistics and group maxima per segment */
     SV_K_LOGPROB_MERGE = 23, /* segments joined: log probabilities, entropy, alternatives */
     SV_K_COUNT = 24
 } sv_kernel_id;
