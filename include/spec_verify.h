@@ -487,7 +487,7 @@ sv_status spec_commit_tree_kv_paged(void *pages, float *scales, int G, int num_p
  * -inf have probability 0; a row of nothing else has entropy 0.  A row that holds
  * a NaN or +inf has no probabilities: its logprob, entropy and top_logprobs are NaN,
  * and its ids are those of its largest logits that are not NaN (-1, with -inf, where
- * it has fewer).
+ * it has fewer; beside a signalling NaN, of some that are not NaN).
  * Workspace: sv_token_logprobs_workspace_bytes (0 for invalid sizes).
  */
 size_t sv_token_logprobs_workspace_bytes(int R, int V, sv_dtype dt, int top_k);

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import draft_token_verification_04_amd as sv
-from gpu_helpers import f32_to_dev, ints_to_dev, note
+from gpu_helpers import dev, f32_to_dev, ints_to_dev, note
 from oracle import paged
 from paged_helpers import bf16_bits, bits_to_dev
 
@@ -86,3 +86,32 @@ def test_nan_and_inf(dtype, V, copies):
     # with neither tokens nor alternatives
     only = sv.spec_token_logprobs(t)
     assert np.array_equal(np.isnan(only["entropy"].cpu().numpy()), ~fine)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,R", [(40, 6), (9000, 6), (30011, 300)])
+def test_signalling_nan(dtype, V, R):
+    # patterns no arithmetic produces: NaN all the same, and ids of numbers
+    note(f"logprobs signalling NaN {dtype} V={V} R={R}")
+    rng = np.random.default_rng(V)
+    x = bf16_bits(rng.normal(size=(R, V))) if dtype == "bf16" else rng.normal(size=(R, V)).astype(np.float32).view(np.uint32)
+    a, b, c = (0x7f81, 0xff81, 0x7fbf) if dtype == "bf16" else (0x7f800001, 0xff800001, 0x7fbfffff)
+    x[1, V // 2], x[2], x[3, ::2], x[4, V // 2:] = a, b, c, a
+    if dtype == "bf16":
+        t, v = bits_to_dev(x), paged.bf16_values(x)
+    else:
+        t = torch.from_numpy(x.view(np.int32)).to(dev()).view(torch.float32)
+        with np.errstate(invalid="ignore"):
+            v = x.view(np.float32).astype(np.float64)
+    g = sv.spec_token_logprobs(t, ints_to_dev(np.zeros(R)), top_k=5)
+    torch.cuda.synchronize()
+    bad = np.isnan(v).any(1)
+    assert bad[1:5].all() and bad.sum() == 4
+    for n in ("logprob", "entropy"):
+        assert np.array_equal(np.isnan(g[n].cpu().numpy()), bad)
+    ids = g["top_ids"].cpu().numpy()
+    for r in range(R):
+        got = ids[r][ids[r] >= 0]
+        assert not np.isnan(v[r, got]).any() and len(set(got.tolist())) == len(got)
+        if not bad[r]:
+            assert np.array_equal(ids[r], np.lexsort((np.arange(V), -v[r]))[:5])
