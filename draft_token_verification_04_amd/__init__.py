@@ -21,6 +21,10 @@ Entry points (same names as the C ABI):
   and cache write of a window), ``spec_attend_paged`` (its attention),
   ``spec_commit_tree_kv_paged``
 * ``spec_token_logprobs`` (log probabilities, entropy, alternatives)
+* for prompts: ``spec_append_kv_packed`` and ``spec_attend_packed`` (cache write and
+  causal attention of packed sequences), ``spec_rms_norm`` (norm with the residual's
+  addition, to bf16 or e4m3) and ``spec_linear_e4m3`` (product of e4m3 operands with
+  block scales)
 """
 
 from __future__ import annotations
@@ -40,10 +44,15 @@ SV_F32, SV_BF16, SV_E4M3 = 0, 1, 2
 SV_MAX_TREE_NODES = 2048
 SV_MAX_WINDOW = 64
 SV_MAX_TOP = 32
+SV_MAX_NORM_COLS = 16384
+SV_MAX_LINEAR_K = 131072
+SV_MAX_AXES = 4
+SCALE_BLOCK = 128
 KERNELS = ("rowstats", "accept", "resid_mass", "resid_select", "argmax", "match", "tree",
            "skip_stats", "skip_argmax", "commit", "lmhead", "ngram_count", "ngram_emit",
            "skip_tree", "read_probe", "lmhead_stats", "lmhead_rows", "merge_parts",
-           "append_paged", "attend", "attend_join", "commit_paged", "logprob", "logprob_merge")
+           "append_paged", "attend", "attend_join", "commit_paged", "logprob", "logprob_merge",
+           "rms_norm", "linear", "linear_join", "append_packed", "attend_packed", "attend_packed_join")
 
 EXPORTS = ("sv_sample_workspace_bytes", "sv_greedy_workspace_bytes", "spec_verify_sample",
            "spec_verify_greedy", "spec_verify_tree", "spec_commit_tree_kv", "sv_status_string",
@@ -52,7 +61,8 @@ EXPORTS = ("sv_sample_workspace_bytes", "sv_greedy_workspace_bytes", "spec_verif
            "sv_read_probe", "sv_read_probe_folds", "sv_trace_begin", "sv_trace_end", "sv_kernel_name",
            "sv_sample_lmhead_workspace_bytes", "spec_verify_sample_lmhead", "spec_verify_sample_noalloc",
            "spec_append_kv_paged", "sv_attend_workspace_bytes", "spec_attend_paged", "spec_commit_tree_kv_paged",
-           "sv_token_logprobs_workspace_bytes", "spec_token_logprobs")
+           "sv_token_logprobs_workspace_bytes", "spec_token_logprobs", "spec_rms_norm", "sv_linear_workspace_bytes",
+           "spec_linear_e4m3", "spec_append_kv_packed", "sv_attend_packed_workspace_bytes", "spec_attend_packed")
 
 
 class SpecVerifyError(RuntimeError):
@@ -125,6 +135,18 @@ def load_library(path: str = LIB_PATH):
     lib.sv_token_logprobs_workspace_bytes.restype = Z
     lib.spec_token_logprobs.argtypes = [P, P, I, I, I, F, I, P, P, P, P, P, P, Z, P]
     lib.spec_token_logprobs.restype = I
+    lib.spec_rms_norm.argtypes = [P, L, P, P, F, I, I, P, P, I, P, P]
+    lib.spec_rms_norm.restype = I
+    lib.sv_linear_workspace_bytes.argtypes = [I, I, I, I]
+    lib.sv_linear_workspace_bytes.restype = Z
+    lib.spec_linear_e4m3.argtypes = [P, L, P, L, P, P, I, I, I, P, I, P, Z, P]
+    lib.spec_linear_e4m3.restype = I
+    lib.spec_append_kv_packed.argtypes = [P, P, P, L, L, L, P, P, F, P, I, I, I, P, I, P, P, P, I, I, I, KV, P, I, P, P, P]
+    lib.spec_append_kv_packed.restype = I
+    lib.sv_attend_packed_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    lib.sv_attend_packed_workspace_bytes.restype = Z
+    lib.spec_attend_packed.argtypes = [P, L, KV, P, I, P, P, I, I, I, F, P, P, P, P, Z, P]
+    lib.spec_attend_packed.restype = I
     lib.sv_read_probe.argtypes = [P, Z, P, P]
     lib.sv_read_probe.restype = I
     lib.sv_read_probe_folds.argtypes = [Z]
@@ -857,6 +879,226 @@ def spec_token_logprobs(logits, tokens=None, *, temperature=1.0, top_k=0, entrop
         raise SpecVerifyError(rc, "spec_token_logprobs")
     _hold(torch, dev, stream, ws if workspace is None else None, *out.values())
     return out
+
+
+# ---- prompts and e4m3 projections --------------------------------------------------
+
+def _matrix(torch, t, name, dtype, dev=None, shape=None):
+    """[rows, columns] whose rows are contiguous and equally far apart; returns that
+    distance."""
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0) if rows > 1 else cols
+
+
+def spec_rms_norm(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, e4m3=False, out=None, stream=None):
+    """RMS norm of the rows of x [T, D] bf16 (rows contiguous, equally far apart), with
+    weight [D] bf16 and the residual's addition: h = x + residual, y = h / sqrt(mean(h^2)
+    + eps) * weight.  D a multiple of 8, at most 16384.
+
+    Returns ``out`` [T, D]: y in bf16, or with e4m3=True in float8_e4m3fn beside
+    ``scales`` [ceil(D / 128), T] float32, one for each row and 128 columns; and with
+    ``residual`` [T, D] bf16, ``residual`` [T, D]: h in bf16 (``residual_out`` if given,
+    which may be ``residual`` itself)."""
+    torch = _torch()
+    lib = load_library()
+    xs = _matrix(torch, x, "x", torch.bfloat16)
+    dev = x.device
+    T, D = x.shape
+    if weight is not None:
+        _check(weight, "weight", 1, torch.bfloat16, dev)
+        if weight.shape[0] != D:
+            raise ValueError(f"weight must be [{D}]")
+    res = {}
+    if residual is not None:
+        _check(residual, "residual", 2, torch.bfloat16, dev)
+        if tuple(residual.shape) != (T, D):
+            raise ValueError(f"residual must be [{T}, {D}]")
+        res["residual"] = _window_out(torch, residual_out, "residual_out", (T, D), torch.bfloat16, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    res["out"] = _window_out(torch, out, "out", (T, D), torch.float8_e4m3fn if e4m3 else torch.bfloat16, dev)
+    if e4m3:
+        res["scales"] = torch.empty((-(-D // SCALE_BLOCK), T), dtype=torch.float32, device=dev)
+    rc = _call(torch, lib.spec_rms_norm, dev, stream, x.data_ptr(), xs, _ptr(residual), _ptr(weight), float(eps), T, D,
+               _ptr(res.get("residual")), res["out"].data_ptr(), SV_E4M3 if e4m3 else SV_BF16, _ptr(res.get("scales")))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_rms_norm")
+    _hold(torch, dev, stream, *res.values())
+    return res
+
+
+@functools.lru_cache(maxsize=4096)
+def linear_workspace_bytes(M, N, K, dtype_code) -> int:
+    return int(load_library().sv_linear_workspace_bytes(M, N, K, dtype_code))
+
+
+def spec_linear_e4m3(x, x_scales, w, w_scales, *, out=None, out_dtype=None, workspace=None, stream=None):
+    """x @ w.T of e4m3 operands with a scale for each block of 128: x [M, K]
+    float8_e4m3fn (rows contiguous, equally far apart) with x_scales [ceil(K / 128), M]
+    float32 (as spec_rms_norm returns them; a slice of columns will do), w [N, K]
+    float8_e4m3fn with w_scales [ceil(N / 128), ceil(K / 128)] float32.  K a multiple of
+    16.  Returns [M, N] in out_dtype (bfloat16 or float32; bfloat16 by default), or
+    ``out``."""
+    torch = _torch()
+    lib = load_library()
+    e4m3 = torch.float8_e4m3fn
+    xs = _matrix(torch, x, "x", e4m3)
+    dev = x.device
+    M, K = x.shape
+    _check(w, "w", 2, e4m3, dev)
+    N, blocks = w.shape[0], -(-K // SCALE_BLOCK)
+    if w.shape[1] != K:
+        raise ValueError(f"w must be [N, {K}], got {list(w.shape)}")
+    ss = _matrix(torch, x_scales, "x_scales", torch.float32, dev, (blocks, M))
+    _check(w_scales, "w_scales", 2, torch.float32, dev)
+    if tuple(w_scales.shape) != (-(-N // SCALE_BLOCK), blocks):
+        raise ValueError(f"w_scales must be [{-(-N // SCALE_BLOCK)}, {blocks}]")
+    if out is not None:
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out must be bfloat16 or float32, got {out_dtype}")
+    out = _window_out(torch, out, "out", (M, N), out_dtype, dev)
+    dt = SV_F32 if out_dtype == torch.float32 else SV_BF16
+    ws = _workspace(torch, linear_workspace_bytes(M, N, K, dt), dev, workspace)
+    rc = _call(torch, lib.spec_linear_e4m3, dev, stream, x.data_ptr(), xs, x_scales.data_ptr(), ss, w.data_ptr(),
+               w_scales.data_ptr(), M, N, K, out.data_ptr(), dt,
+               ws.data_ptr(), ws.numel() * ws.element_size())
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_linear_e4m3")
+    _hold(torch, dev, stream, ws if workspace is None else None, out)
+    return out
+
+
+def _packed_rows(torch, t, name, heads, head_dim, dev, tokens=None):
+    """[T, heads, head_dim] bf16 whose heads are consecutive; returns the distance of
+    its tokens."""
+    if t is None or t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    T, H, D = t.shape
+    if D != head_dim or (heads is not None and H != heads) or (tokens is not None and T != tokens):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be consecutive")
+    return st if T > 1 else H * D
+
+
+def _packed_bounds(torch, page_table, starts, base, dev):
+    _check(page_table, "page_table", 2, torch.int32, dev)
+    B, P = page_table.shape
+    _window_ints(torch, starts, "starts", (B + 1,), dev)
+    if starts is None:
+        raise ValueError("starts is required")
+    _window_ints(torch, base, "base", (B,), dev)
+    return B, P
+
+
+def spec_append_kv_packed(q, k, v, cache, page_table, starts, base=None, positions=None, *, q_weight=None,
+                          k_weight=None, eps=1e-6, rope=None, interleaved=False, pair_axis=None, q_out=None,
+                          status=True, stream=None):
+    """spec_append_kv_paged for packed sequences: q [T, H, head_dim], k and v [T,
+    kv_heads, head_dim] bf16 (slices of a projection's output), the tokens of request b
+    being starts[b] ... starts[b + 1] - 1 (starts [B + 1] int32, rising), behind base[b]
+    cached ones (base [B] int32; None: none).
+
+    positions [T] or [axes, T] int32 (axes <= 4); pair_axis [rot / 2] int32 names the
+    axis whose position turns each pair of a head.  Returns ``q`` [T, H, head_dim] bf16
+    (``q_out`` if given; tokens outside every request are left as they were) and
+    ``status`` [T]."""
+    torch = _torch()
+    lib = load_library()
+    dev, D = cache.device, cache.head_dim
+    qs = _packed_rows(torch, q, "q", None, D, dev)
+    T, H, _ = q.shape
+    ks = _packed_rows(torch, k, "k", cache.kv_heads, D, dev, T)
+    vs = _packed_rows(torch, v, "v", cache.kv_heads, D, dev, T)
+    B, P = _packed_bounds(torch, page_table, starts, base, dev)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check(w, name, 1, torch.bfloat16, dev)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must be [{D}]")
+    rot = max_pos = 0
+    axes = 1
+    if rope is not None:
+        _check(rope, "rope", 2, torch.float32, dev)
+        max_pos, rot = rope.shape
+        if positions is None:
+            raise ValueError("positions is required with rope")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        _window_ints(torch, positions, "positions", (axes, T) if positions.dim() == 2 else (T,), dev)
+        if axes > 1 and pair_axis is None:
+            raise ValueError("pair_axis is required with positions of several axes")
+        _window_ints(torch, pair_axis, "pair_axis", (rot // 2,), dev)
+    res = dict(q=_window_out(torch, q_out, "q_out", (T, H, D), torch.bfloat16, dev))
+    if status:
+        res["status"] = torch.empty(T, dtype=torch.int32, device=dev)
+    rc = _call(
+        torch, lib.spec_append_kv_packed, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope), rot, max_pos, int(bool(interleaved)),
+        _ptr(positions if rope is not None else None), axes, _ptr(pair_axis if rope is not None else None),
+        starts.data_ptr(), _ptr(base), T, B, H, cache._c, page_table.data_ptr(), P, res["q"].data_ptr(),
+        _ptr(res.get("status")))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_append_kv_packed")
+    _hold(torch, dev, stream, *res.values())
+    return res
+
+
+@functools.lru_cache(maxsize=4096)
+def attend_packed_workspace_bytes(T, B, H, kv_heads, head_dim, P, page_size) -> int:
+    return int(load_library().sv_attend_packed_workspace_bytes(T, B, H, kv_heads, head_dim, P, page_size))
+
+
+def spec_attend_packed(q, cache, page_table, starts, base=None, *, scale=None, out=None, lse=False, status=True,
+                       workspace=None, stream=None):
+    """Causal attention of packed sequences over ``cache`` (a PagedKV that already holds
+    their keys and values): q [T, H, head_dim] bf16, the tokens of request b being
+    starts[b] ... starts[b + 1] - 1 (starts [B + 1] int32), behind base[b] cached ones
+    (base [B] int32; None: none).  Token starts[b] + j sees the slots below base[b] + j
+    + 1; scale defaults to head_dim ** -0.5.
+
+    Returns ``out`` [T, H, head_dim] bf16, ``lse`` [T, H] float32 (lse=True, or a tensor
+    to write) and ``status`` [B].  Rows of tokens outside every request are left as they
+    were in ``out`` and ``lse``."""
+    torch = _torch()
+    lib = load_library()
+    dev, D = cache.device, cache.head_dim
+    qs = _packed_rows(torch, q, "q", None, D, dev)
+    T, H, _ = q.shape
+    B, P = _packed_bounds(torch, page_table, starts, base, dev)
+    res = dict(out=_window_out(torch, out, "out", (T, H, D), torch.bfloat16, dev))
+    if lse is not False and lse is not None:
+        res["lse"] = _window_out(torch, None if lse is True else lse, "lse", (T, H), torch.float32, dev)
+    if status:
+        res["status"] = torch.empty(B, dtype=torch.int32, device=dev)
+    ws = _workspace(torch, attend_packed_workspace_bytes(T, B, H, cache.kv_heads, D, P, cache.page_size), dev, workspace)
+    rc = _call(
+        torch, lib.spec_attend_packed, dev, stream, q.data_ptr(), qs, cache._c, page_table.data_ptr(), P,
+        starts.data_ptr(), _ptr(base), T, B, H, float(D ** -0.5 if scale is None else scale), res["out"].data_ptr(),
+        _ptr(res.get("lse")), _ptr(res.get("status")), ws.data_ptr(), ws.numel() * ws.element_size())
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_attend_packed")
+    _hold(torch, dev, stream, ws if workspace is None else None, *res.values())
+    return res
 
 
 def sv_read_probe(buf, *, folds=None, stream=None):

@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = ["sv_api.hip", "sv_sample.hip", "sv_greedy.hip", "sv_commit.hip", "sv_lmhead.hip",
            "sv_ngram.hip", "sv_probe.hip", "sv_append.hip", "sv_attend.hip", "sv_commit_paged.hip",
-           "sv_logprob.hip"]
+           "sv_logprob.hip", "sv_norm.hip", "sv_linear.hip", "sv_attend_packed.hip"]
 ARCH = "gfx950"
 
 

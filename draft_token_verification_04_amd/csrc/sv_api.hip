@@ -11,6 +11,7 @@
 #include "sv_device.hpp"
 #include "sv_internal.hpp"
 #include "sv_paged_internal.hpp"
+#include "sv_prompt_internal.hpp"
 #include "sv_skip.hpp"
 
 namespace sv {
@@ -921,6 +922,227 @@ sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, 
 
 }  // extern "C"
 
+// ---- prompts and e4m3 projections ------------------------------------------------------
+
+namespace {
+
+// The tokens' strides of a packed or windowed append, in elements.
+bool stride_ok(long long stride, long long least, bool several) {
+    return stride % 8 == 0 && (stride >= least || !several);
+}
+
+bool packed_sizes_ok(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size) {
+    if (!paged_sizes_ok(page_size, head_dim) || static_cast<long long>(P) * page_size > kMaxSlots) return false;
+    if (H > 65536 || static_cast<double>(T) * H > 2.0e9) return false;
+    if (B == 0) return true;
+    const PackedPlan p = packed_plan(T, B, H, kv_heads, head_dim, P, page_size);
+    return packed_groups(kv_heads, p) <= kMaxGroups && packed_join_groups(kv_heads, head_dim, p) <= kMaxGroups;
+}
+
+}  // namespace
+
+extern "C" {
+
+sv_status spec_rms_norm(const void *x, long long x_stride, const void *residual, const void *weight, float eps, int T,
+                        int D, void *residual_out, void *out, sv_dtype out_dt, float *out_scale, hipStream_t stream) {
+    if (out_dt != SV_BF16 && out_dt != SV_E4M3) return SV_ERR_UNSUPPORTED;
+    if (T < 0 || D < 1 || !(eps >= 0.0f) || !isfinite(eps)) return SV_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > SV_MAX_NORM_COLS || T > kMaxGroups) return SV_ERR_UNSUPPORTED;
+    if (T == 0) return SV_OK;
+    if (!x || !out || (out_dt == SV_E4M3) != (out_scale != nullptr)) return SV_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(out) ||
+        !aligned16(out_scale))
+        return SV_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, D, T > 1)) return SV_ERR_INVALID_ARG;
+    if (x_stride > 1LL << 31) return SV_ERR_UNSUPPORTED;
+    NormArgs a = {};
+    a.x = static_cast<const uint16_t *>(x);
+    a.x_stride = x_stride;
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.weight = static_cast<const uint16_t *>(weight);
+    a.eps = eps;
+    a.T = T;
+    a.D = D;
+    a.residual_out = static_cast<uint16_t *>(residual_out);
+    a.out = out;
+    a.out_scale = out_scale;
+    const hipError_t e = traced(SV_K_RMS_NORM, stream, [&] { return launch_rms_norm(a, out_dt == SV_E4M3, stream); });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+size_t sv_linear_workspace_bytes(int M, int N, int K, sv_dtype out_dt) {
+    if (!valid_dtype(out_dt) || M < 1 || N < 1 || K < 1 || K % 16 != 0 || K > SV_MAX_LINEAR_K) return 0;
+    const LinearPlan p = linear_plan(M, N, K, out_dt == SV_F32);
+    if (p.groups > kMaxGroups) return 0;
+    return std::max<size_t>(256, p.total);
+}
+
+sv_status spec_linear_e4m3(const void *x, long long x_stride, const float *x_scale, long long x_scale_stride,
+                           const void *w, const float *w_scale, int M, int N, int K, void *out, sv_dtype out_dt,
+                           void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!valid_dtype(out_dt)) return SV_ERR_UNSUPPORTED;
+    if (M < 0 || N < 1 || K < 1) return SV_ERR_INVALID_ARG;
+    if (K % 16 != 0 || K > SV_MAX_LINEAR_K) return SV_ERR_UNSUPPORTED;
+    if (M == 0) return SV_OK;
+    const LinearPlan p = linear_plan(M, N, K, out_dt == SV_F32);
+    if (p.groups > kMaxGroups) return SV_ERR_UNSUPPORTED;
+    if (!x || !x_scale || !w || !w_scale || !out || !workspace) return SV_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(out) || !aligned256(workspace)) return SV_ERR_INVALID_ARG;
+    if (x_stride % 16 != 0 || (x_stride < K && M > 1) || x_scale_stride < M) return SV_ERR_INVALID_ARG;
+    if (x_stride > 1LL << 31 || x_scale_stride > 1LL << 31) return SV_ERR_UNSUPPORTED;
+    if (workspace_bytes < std::max<size_t>(256, p.total)) return SV_ERR_WORKSPACE;
+    LinearArgs a = {};
+    a.x = static_cast<const uint8_t *>(x);
+    a.x_stride = x_stride;
+    a.x_scale = x_scale;
+    a.x_scale_stride = x_scale_stride;
+    a.w = static_cast<const uint8_t *>(w);
+    a.w_scale = w_scale;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.out = out;
+    a.part = static_cast<float *>(workspace);
+    a.splits = p.splits;
+    const bool f32 = out_dt == SV_F32;
+    hipError_t e = traced(SV_K_LINEAR, stream, [&] { return launch_linear(a, p, f32, stream); });
+    if (e == hipSuccess && p.splits > 1)
+        e = traced(SV_K_LINEAR_JOIN, stream, [&] { return launch_linear_join(a, f32, stream); });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, long long q_stride, long long k_stride,
+                                long long v_stride, const void *q_weight, const void *k_weight, float eps,
+                                const float *rope, int rot, int max_pos, int interleaved, const int32_t *positions,
+                                int axes, const int32_t *pair_axis, const int32_t *starts, const int32_t *base, int T,
+                                int B, int H, sv_paged_kv cache, const int32_t *page_table, int P, void *q_out,
+                                int32_t *token_status, hipStream_t stream) {
+    sv_status st = check_cache(cache, P);
+    if (st != SV_OK) return st;
+    if (T < 0 || B < 0 || H < 1 || !(eps >= 0.0f) || !isfinite(eps)) return SV_ERR_INVALID_ARG;
+    const int D = cache.head_dim;
+    if (rope) {
+        if (rot < 1 || rot > D || max_pos < 1 || axes < 1 || (axes > 1 && !pair_axis)) return SV_ERR_INVALID_ARG;
+        if (rot % 16 != 0 || axes > SV_MAX_AXES) return SV_ERR_UNSUPPORTED;
+    }
+    if (T > kMaxGroups || static_cast<long long>(H) + 2LL * cache.kv_heads > 65536 || B == 0x7fffffff)
+        return SV_ERR_UNSUPPORTED;
+    if (T == 0) return SV_OK;
+    if (!q || !k || !v || !starts || (B > 0 && !page_table) || !q_out || (rope && !positions)) return SV_ERR_INVALID_ARG;
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return SV_ERR_INVALID_ARG;
+    st = check_cache_pointers(cache);
+    if (st != SV_OK) return st;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope) ||
+        !aligned16(q_weight) || !aligned16(k_weight))
+        return SV_ERR_INVALID_ARG;
+    const long long kv_row = static_cast<long long>(cache.kv_heads) * D;
+    if (!stride_ok(q_stride, static_cast<long long>(H) * D, T > 1) || !stride_ok(k_stride, kv_row, T > 1) ||
+        !stride_ok(v_stride, kv_row, T > 1))
+        return SV_ERR_INVALID_ARG;
+    if (q_stride > 1LL << 31 || k_stride > 1LL << 31 || v_stride > 1LL << 31) return SV_ERR_UNSUPPORTED;
+    AppendArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_weight = static_cast<const uint16_t *>(q_weight);
+    a.k_weight = static_cast<const uint16_t *>(k_weight);
+    a.eps = eps;
+    a.rope = rope;
+    a.rot = rope ? rot : 0;
+    a.max_pos = max_pos;
+    a.interleaved = interleaved != 0;
+    a.positions = positions;
+    a.base = base;
+    a.page_table = page_table;
+    a.N = 1;
+    a.H = H;
+    a.Hkv = cache.kv_heads;
+    a.P = P;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(cache.page_size));
+    a.num_pages = cache.num_pages;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.k_pages = cache.k;
+    a.v_pages = cache.v;
+    a.k_scale = cache.k_scale;
+    a.v_scale = cache.v_scale;
+    a.status = token_status;
+    a.starts = starts;
+    a.pair_axis = pair_axis;
+    a.B = B;
+    a.T = T;
+    a.axes = axes;
+    const hipError_t e = traced(SV_K_APPEND_PACKED, stream,
+                                [&] { return launch_append(a, D, cache.dt == SV_E4M3, T, stream); });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+size_t sv_attend_packed_workspace_bytes(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size) {
+    if (T < 0 || B < 1 || H < 1 || kv_heads < 1 || P < 1 || H % kv_heads != 0 ||
+        !packed_sizes_ok(T, B, H, kv_heads, head_dim, P, page_size))
+        return 0;
+    return std::max<size_t>(256, packed_plan(T, B, H, kv_heads, head_dim, P, page_size).total);
+}
+
+sv_status spec_attend_packed(const void *q, long long q_stride, sv_paged_kv cache, const int32_t *page_table, int P,
+                             const int32_t *starts, const int32_t *base, int T, int B, int H, float scale, void *out,
+                             float *lse, int32_t *req_status, void *workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    sv_status st = check_cache(cache, P);
+    if (st != SV_OK) return st;
+    if (T < 0 || B < 0 || H < 1 || H % cache.kv_heads != 0 || !(scale > 0.0f) || !isfinite(scale))
+        return SV_ERR_INVALID_ARG;
+    const int D = cache.head_dim;
+    if (!packed_sizes_ok(T, B, H, cache.kv_heads, D, P, cache.page_size)) return SV_ERR_UNSUPPORTED;
+    if (B == 0) return SV_OK;
+    if (!page_table || !starts || (T > 0 && (!q || !out)) || !workspace) return SV_ERR_INVALID_ARG;
+    st = check_cache_pointers(cache);
+    if (st != SV_OK) return st;
+    if (!aligned16(q) || !aligned16(out) || !aligned256(workspace)) return SV_ERR_INVALID_ARG;
+    if (!stride_ok(q_stride, static_cast<long long>(H) * D, T > 1)) return SV_ERR_INVALID_ARG;
+    if (q_stride > 1LL << 31) return SV_ERR_UNSUPPORTED;
+    const PackedPlan p = packed_plan(T, B, H, cache.kv_heads, D, P, cache.page_size);
+    if (workspace_bytes < std::max<size_t>(256, p.total)) return SV_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    PackedArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.q_stride = q_stride;
+    a.k_pages = cache.k;
+    a.v_pages = cache.v;
+    a.k_scale = cache.k_scale;
+    a.v_scale = cache.v_scale;
+    a.page_table = page_table;
+    a.starts = starts;
+    a.base = base;
+    a.T = T;
+    a.B = B;
+    a.H = H;
+    a.Hkv = cache.kv_heads;
+    a.G = H / cache.kv_heads;
+    a.P = P;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(cache.page_size));
+    a.num_pages = cache.num_pages;
+    a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634073599246810018921);
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.status = req_status;
+    a.S = p.S;
+    a.units = p.units;
+    a.part_o = reinterpret_cast<float *>(ws + p.part_o);
+    a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
+    a.part_bad = reinterpret_cast<int32_t *>(ws + p.part_bad);
+    if (!isfinite(a.c)) return SV_ERR_UNSUPPORTED;
+    const bool e4m3 = cache.dt == SV_E4M3;
+    hipError_t e = traced(SV_K_ATTEND_PACKED, stream, [&] { return launch_attend_packed(a, D, e4m3, p, stream); });
+    if (e == hipSuccess && p.S > 1)
+        e = traced(SV_K_ATTEND_PACKED_JOIN, stream, [&] { return launch_attend_packed_join(a, D, p, stream); });
+    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+}  // extern "C"
+
 extern "C" {
 
 size_t sv_read_probe_folds(size_t bytes) {
@@ -960,7 +1182,9 @@ const char *sv_kernel_name(int k) {
                                             "skip_argmax", "commit", "lmhead", "ngram_count",
                                             "ngram_emit", "skip_tree", "read_probe", "lmhead_stats",
                                             "lmhead_rows", "merge_parts", "append_paged", "attend",
-                                            "attend_join", "commit_paged", "logprob", "logprob_merge"};
+                                            "attend_join", "commit_paged", "logprob", "logprob_merge",
+                                            "rms_norm", "linear", "linear_join", "append_packed",
+                                            "attend_packed", "attend_packed_join"};
     return (k >= 0 && k < SV_K_COUNT) ? names[k] : "unknown";
 }
 

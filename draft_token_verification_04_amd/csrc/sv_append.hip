@@ -17,6 +17,12 @@
 // the maximum and the half-split rotation's partners move between the lanes of
 // a row.  A workgroup takes one token: its lanes keep the token's angles in
 // registers over all the rows they walk.
+//
+// Packed sequences (PACKED): token t belongs to the request b with starts[b] <= t <
+// starts[b + 1], found by a wave that reads 64 starts at a time, and pair i of the
+// rotation turns by the position on axis pair_axis[i] (images and video have
+// positions of time, height and width), so a lane reads its angles from as many
+// rows of the table as its pairs have axes.
 #include "sv_paged.hpp"
 #include "sv_paged_internal.hpp"
 
@@ -36,19 +42,28 @@ __device__ __forceinline__ float row_max(float v) {
     return v;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PACKED>
 __global__ __launch_bounds__(kBlock) void k_append(AppendArgs a) {
     constexpr int kLanes = D / 8;                 // lanes per row
     constexpr int kRows = kBlock / kLanes;        // rows a workgroup holds at once
     const int tok = blockIdx.x;
-    const int b = tok / a.N, j = tok - b * a.N;
     const bool first = blockIdx.y == 0 && threadIdx.x == 0;
-    if (j >= window_rows(a.counts, b, a.N)) {  // padding: nothing is written
+    int b, j;
+    bool there;
+    if constexpr (PACKED) {
+        b = uniform(last_not_above(a.starts, a.B + 1, tok, threadIdx.x & (kWave - 1)));
+        there = b >= 0 && b < a.B;
+        j = there ? tok - a.starts[b] : 0;
+    } else {
+        b = tok / a.N, j = tok - b * a.N;
+        there = j < window_rows(a.counts, b, a.N);
+    }
+    if (!there) {  // padding: nothing is written
         if (first && a.status) a.status[tok] = 0;
         return;
     }
     // where the token goes; a bad slot, page or position writes nothing
-    const long long slot = static_cast<long long>(a.base[b]) + j;
+    const long long slot = static_cast<long long>(PACKED && !a.base ? 0 : a.base[b]) + j;
     const int pos = a.rope ? a.positions[tok] : 0;
     int page = -1;
     if (slot >= 0 && (slot >> a.page_shift) < a.P)
@@ -58,6 +73,19 @@ __global__ __launch_bounds__(kBlock) void k_append(AppendArgs a) {
         code = 1;
     else if (a.rope && (pos < 0 || pos >= a.max_pos))
         code = 2;
+    if constexpr (PACKED) {
+        // the other axes' positions (a few), and the axes of the pairs
+        for (int x = 1; a.rope && x < a.axes; ++x) {
+            const int p = a.positions[static_cast<long long>(x) * a.T + tok];
+            if (code == 0 && (p < 0 || p >= a.max_pos)) code = 2;
+        }
+        if (a.rope && a.pair_axis) {
+            bool bad = false;
+            for (int i = threadIdx.x & (kWave - 1); i < a.rot / 2; i += kWave)
+                bad |= a.pair_axis[i] < 0 || a.pair_axis[i] >= a.axes;
+            if (code == 0 && ballot(bad) != 0) code = 2;
+        }
+    }
     if (first && a.status) a.status[tok] = code;
     if (code) return;
     const int in_page = static_cast<int>(slot & ((1 << a.page_shift) - 1));
@@ -72,7 +100,21 @@ __global__ __launch_bounds__(kBlock) void k_append(AppendArgs a) {
     const bool upper = d0 >= half;  // half split: holds the second value of its pairs
     if (turned) {
         const float *t = a.rope + static_cast<long long>(pos) * a.rot;
-        if (a.interleaved) {
+        if (PACKED && a.pair_axis) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (a.interleaved && e % 2) {
+                    cs[e] = cs[e - 1];
+                    sn[e] = sn[e - 1];
+                    continue;
+                }
+                const int i = a.interleaved ? (d0 + e) / 2 : (upper ? d0 - half : d0) + e;
+                const long long at = static_cast<long long>(a.pair_axis[i]) * a.T + tok;
+                const float *r = a.rope + static_cast<long long>(a.positions[at]) * a.rot;
+                cs[e] = r[i];
+                sn[e] = r[half + i];
+            }
+        } else if (a.interleaved) {
             const float4 x = *reinterpret_cast<const float4 *>(t + d0 / 2);
             const float4 y = *reinterpret_cast<const float4 *>(t + half + d0 / 2);
             cs[0] = cs[1] = x.x, cs[2] = cs[3] = x.y, cs[4] = cs[5] = x.z, cs[6] = cs[7] = x.w;
@@ -165,10 +207,14 @@ __global__ __launch_bounds__(kBlock) void k_append(AppendArgs a) {
     }
 }
 
+template <int D, bool PACKED>
+hipError_t launch_packed(const AppendArgs &a, bool e4m3, dim3 grid, hipStream_t s) {
+    return e4m3 ? launch_kernel(k_append<D, true, PACKED>, grid, dim3(kBlock), 0, s, a)
+                : launch_kernel(k_append<D, false, PACKED>, grid, dim3(kBlock), 0, s, a);
+}
 template <int D>
 hipError_t launch_d(const AppendArgs &a, bool e4m3, dim3 grid, hipStream_t s) {
-    return e4m3 ? launch_kernel(k_append<D, true>, grid, dim3(kBlock), 0, s, a)
-                : launch_kernel(k_append<D, false>, grid, dim3(kBlock), 0, s, a);
+    return a.starts ? launch_packed<D, true>(a, e4m3, grid, s) : launch_packed<D, false>(a, e4m3, grid, s);
 }
 
 }  // namespace

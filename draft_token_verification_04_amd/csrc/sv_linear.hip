@@ -1,0 +1,501 @@
+// sv_linear.hip -- matrix product of e4m3 operands with a scale for each block of
+// 128:  out[m][n] = sum_b xs[b][m] ws[n / 128][b] sum_{k in b} x[m][k] w[n][k],
+// b the blocks of 128 columns; x is scaled by row and block, w by block of 128 x 128.
+//
+// A block's products are summed on the matrix cores; the sum enters an fp32
+// accumulator by one fma with the product of the two scales.  For bf16 outputs the sum
+// is one v_mfma_f32_16x16x128_f8f6f4, whose depth is one block.  The e4m3 matrix
+// instructions align a sum's products to the largest with few bits to spare: on
+// Gaussian operands the sums of 128 are 1.5e-5 off (relative, root mean square), far
+// below bf16's rounding but far above fp32's.  For fp32 outputs both operands are
+// therefore widened to bf16 (exactly), whose products and sums are good to 1e-8, at half
+// the rate.
+//
+// W is the left operand and the tokens are the right one's columns: a lane then holds
+// four outputs of one token, whose scale is one register, beside W's, which is uniform.
+// The order of a lane's 32 values of a block is the same for both operands, so any
+// order will do: lane group g takes the 16-byte chunks g and g + 4.
+#include <algorithm>
+
+#include "sv_paged.hpp"
+#include "sv_prompt_internal.hpp"
+
+namespace sv {
+namespace {
+
+#define SV_LDS __attribute__((address_space(3)))
+#define SV_GLOBAL __attribute__((address_space(1)))
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+__device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
+
+// A lane's 32 values of a block as an operand: e4m3, or (WIDE) widened to bf16.
+template <bool WIDE>
+struct Operand;
+template <>
+struct Operand<false> {
+    i32x8 v;
+    __device__ __forceinline__ void set(const u32x4 &lo, const u32x4 &hi) {
+        v = i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
+                  static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+    }
+};
+template <>
+struct Operand<true> {
+    bf16x8 v[4];
+    __device__ __forceinline__ void set(const u32x4 &lo, const u32x4 &hi) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned a = i < 2 ? lo[2 * i] : hi[2 * i - 4], b = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+            const u32x4 w = {e4m3_to_bf16<false>(a), e4m3_to_bf16<true>(a), e4m3_to_bf16<false>(b), e4m3_to_bf16<true>(b)};
+            v[i] = __builtin_bit_cast(bf16x8, w);
+        }
+    }
+};
+// 16 x 16 sums over one block, from zero.
+__device__ __forceinline__ f32x4 block_sum(const Operand<false> &a, const Operand<false> &b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 block_sum(const Operand<true> &a, const Operand<true> &b) {
+    f32x4 c = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
+    return c;
+}
+
+// Outputs n .. n + 3 of token m (whole: N is a multiple of 4, so they are all inside
+// and aligned).
+template <bool F32>
+__device__ __forceinline__ void store4(void *out, int N, int m, int n, const f32x4 &v) {
+    const long long at = static_cast<long long>(m) * N + n;
+    const bool whole = (N & 3) == 0;
+    if constexpr (F32) {
+        float *p = static_cast<float *>(out) + at;
+        if (whole) {
+            if (n < N) *reinterpret_cast<f32x4 *>(p) = v;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) p[j] = v[j];
+        }
+    } else {
+        uint16_t *p = static_cast<uint16_t *>(out) + at;
+        const u32x2 w = {pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
+        if (whole) {
+            if (n < N) *reinterpret_cast<u32x2 *>(p) = w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) p[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
+        }
+    }
+}
+
+// ---- few tokens: W is streamed once ------------------------------------------------
+
+// A workgroup takes 16 NT rows of W and up to 16 MT tokens; its waves take every
+// WAVES-th block of K, straight from memory into registers with kDepth blocks in
+// flight, and join their sums through LDS.
+template <int MT, int NT, int WAVES, bool F32>
+__global__ __launch_bounds__(WAVES *kWave) void k_linear_few(LinearArgs a) {
+    constexpr int kDepth = NT * MT >= 8 ? 2 : 4;
+    __shared__ f32x4 sums[WAVES][NT * MT][kWave];
+    const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
+    const int col = lane & 15, kg = lane >> 4;
+    const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
+    const int blocks = (a.K + kScaleBlock - 1) / kScaleBlock;
+    const float *ws = a.w_scale + static_cast<long long>(n0 / kScaleBlock) * blocks;
+
+    const uint8_t *wp[NT], *xp[MT];
+    const float *xs[MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) wp[t] = a.w + static_cast<long long>(min(n0 + 16 * t + col, a.N - 1)) * a.K + kg * 16;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int m = min(m0 + 16 * t + col, a.M - 1);
+        xp[t] = a.x + m * a.x_stride + kg * 16;
+        xs[t] = a.x_scale + m;
+    }
+    struct Block {
+        u32x4 w[NT][2], x[MT][2];
+        float xs[MT], ws;
+    };
+    // what lies behind K is zero in both operands
+    auto load = [&](Block &b, int kb) {
+        const long long k = static_cast<long long>(kb) * kScaleBlock;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const bool in = k + kg * 16 + half * 64 < a.K;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                b.w[t][half] = in ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[t] + k + half * 64)) : u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                b.x[t][half] = in ? *reinterpret_cast<const u32x4 *>(xp[t] + k + half * 64) : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) b.xs[t] = xs[t][kb * a.x_scale_stride];
+        b.ws = ws[kb];
+    };
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0, 0, 0, 0};
+    Block b[kDepth];
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i)
+        if (w + i * WAVES < blocks) load(b[i], w + i * WAVES);
+    for (int kb = w; kb < blocks; kb += kDepth * WAVES) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+            if (kb + i * WAVES >= blocks) break;
+            Operand<F32> wf[NT], xf;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) wf[t].set(b[i].w[t][0], b[i].w[t][1]);
+#pragma unroll
+            for (int u = 0; u < MT; ++u) {
+                xf.set(b[i].x[u][0], b[i].x[u][1]);
+                const float s = b[i].xs[u] * b[i].ws;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t][u] += block_sum(wf[t], xf) * s;
+            }
+            if (kb + (i + kDepth) * WAVES < blocks) load(b[i], kb + (i + kDepth) * WAVES);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) sums[w][t * MT + u][lane] = acc[t][u];
+    __syncthreads();
+    for (int i = w; i < NT * MT; i += WAVES) {
+        f32x4 v = sums[0][i][lane];
+#pragma unroll
+        for (int j = 1; j < WAVES; ++j) v += sums[j][i][lane];
+        const int m = m0 + (i % MT) * 16 + col;
+        if (m < a.M) store4<F32>(a.out, a.N, m, n0 + (i / MT) * 16 + kg * 4, v);
+    }
+}
+
+// ---- many tokens -------------------------------------------------------------------
+
+constexpr int kRowB = kScaleBlock;  // bytes of a slab's row: one block, one cache line
+constexpr int kXcds = 8;
+
+template <int I>
+struct Index {
+    static constexpr int value = I;
+};
+template <int I, int N, typename F>
+__device__ __forceinline__ void unrolled(F &&f) {
+    if constexpr (I < N) {
+        f(Index<I>{});
+        unrolled<I + 1, N>(f);
+    }
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // all but the wave's N youngest
+    static_assert(N < 64, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
+// 16 bytes at LDS address at + OFF; there once a wait for the LDS reads has passed
+// that names the register.
+template <int OFF>
+__device__ __forceinline__ u32x4 lds_read(uint32_t at) {
+    u32x4 r;
+    asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(r) : "v"(at), "i"(OFF));
+    return r;
+}
+
+template <int OFF>
+__device__ __forceinline__ float lds_read_float(uint32_t at) {
+    float r;
+    asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(r) : "v"(at), "i"(OFF));
+    return r;
+}
+// All but the wave's N youngest LDS reads have arrived, these registers among them.
+template <int N>
+__device__ __forceinline__ void arrived(u32x4 &a, u32x4 &b) {
+    asm volatile("s_waitcnt lgkmcnt(%2)" : "+v"(a), "+v"(b) : "i"(N));
+}
+template <int N>
+__device__ __forceinline__ void arrived(float &a) {
+    asm volatile("s_waitcnt lgkmcnt(%1)" : "+v"(a) : "i"(N));
+}
+
+// The shape of a workgroup: WM x WN waves, each with XT tiles of 16 tokens and WT tiles
+// of 16 rows of W, and STAGES stages of LDS.
+template <int WM_, int WN_, int XT_, int WT_, int STAGES_>
+struct Shape {
+    static constexpr int WM = WM_, WN = WN_, XT = XT_, WT = WT_, kStages = STAGES_;
+    static constexpr int kWaves = WM * WN;
+    static constexpr int kTokens = WM * XT * 16, kWRows = WN * WT * 16;
+    static constexpr int kXLoads = kTokens / 8 / kWaves, kWLoads = kWRows / 8 / kWaves;  // 1 KB loads of a wave
+    static constexpr int kLoads = kXLoads + kWLoads + 1;
+    static constexpr int kStageB = (kTokens + kWRows) * kRowB + kWaves * kWave * 4;  // slabs, token scales
+    static constexpr int kLds = kStages * kStageB;
+    static_assert(kTokens % (8 * kWaves) == 0 && kWRows % (8 * kWaves) == 0, "whole loads");
+    static_assert(WT * 16 <= kScaleBlock && kWRows % kScaleBlock == 0, "a wave's rows share a scale");
+};
+
+// A workgroup owns a tile of tokens x rows of W and walks its part of K a block at a
+// time.  Both operands' slabs, and each wave's token scales, go straight from memory to
+// LDS, STAGES - 1 blocks ahead; a slab's row is one cache line, its chunk c stored at
+// c ^ ((r >> 1) & 7), so that the reads of 16 rows meet distinct banks.  The products of
+// one row tile run while the one before enters the accumulators.
+template <typename S, bool F32>
+__global__ __launch_bounds__(S::kWaves *kWave) void k_linear_tile(LinearArgs a, int mtiles, int ntiles) {
+    constexpr int XT = S::XT, WT = S::WT;
+    extern __shared__ __align__(1024) char lds[];  // the stages, then W's scales [WN][blocks]
+    const int bid = blockIdx.x % (mtiles * ((ntiles + kXcds - 1) / kXcds) * kXcds);
+    const int split = blockIdx.x / (mtiles * ((ntiles + kXcds - 1) / kXcds) * kXcds);
+    const int xcd = bid % kXcds, j = bid / kXcds;
+    const int mt = j % mtiles, nt = (j / mtiles) * kXcds + xcd;
+    if (nt >= ntiles) return;
+    const int m0 = mt * S::kTokens, n0 = nt * S::kWRows;
+    const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
+    const int col = lane & 15, kg = lane >> 4;
+    const int wm = w / S::WN, wn = w % S::WN;
+    const int all = (a.K + kScaleBlock - 1) / kScaleBlock, chunks = a.K / 16;
+    const int b0 = static_cast<int>(static_cast<long long>(all) * split / a.splits);
+    const int blocks = static_cast<int>(static_cast<long long>(all) * (split + 1) / a.splits) - b0;
+
+    float *wsc = reinterpret_cast<float *>(lds + S::kLds);
+    for (int i = threadIdx.x; i < S::WN * blocks; i += S::kWaves * kWave) {
+        const int g = i / blocks, kb = i - g * blocks;
+        const int nb = min(n0 + g * WT * 16, a.N - 1) / kScaleBlock;
+        wsc[i] = a.w_scale[static_cast<long long>(nb) * all + b0 + kb];
+    }
+    // load i of wave w fills rows 8 (waves i + w) ... + 7 of a slab; lane l the chunk l % 8
+    const uint8_t *xg[S::kXLoads], *wg[S::kWLoads];
+    auto row_of = [&](int i) { return 8 * (S::kWaves * i + w) + lane / 8; };
+    auto chunk_of = [&](int i) { return (lane % 8) ^ ((row_of(i) >> 1) & 7); };
+#pragma unroll
+    for (int i = 0; i < S::kXLoads; ++i)
+        xg[i] = a.x + min(m0 + row_of(i), a.M - 1) * a.x_stride + b0 * kScaleBlock + chunk_of(i) * 16;
+#pragma unroll
+    for (int i = 0; i < S::kWLoads; ++i)
+        wg[i] = a.w + static_cast<long long>(min(n0 + row_of(i), a.N - 1)) * a.K + b0 * kScaleBlock + chunk_of(i) * 16;
+    const float *xs = a.x_scale + b0 * a.x_scale_stride + min(m0 + wm * XT * 16 + lane % (XT * 16), a.M - 1);
+    auto issue = [&](int s) {
+        char *stage = lds + s % S::kStages * S::kStageB;
+        const bool whole = (b0 + s + 1) * 8 <= chunks;
+        auto from = [&](const uint8_t *p, int i) {  // what lies behind K is zero in both operands
+            if (!whole && (b0 + s) * 8 + chunk_of(i) >= chunks) return reinterpret_cast<const uint8_t *>(&kZeroChunk);
+            return p + s * kScaleBlock;
+        };
+#pragma unroll
+        for (int i = 0; i < S::kXLoads; ++i)
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from(xg[i], i), (SV_LDS void *)(stage + (S::kWaves * i + w) * 1024), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < S::kWLoads; ++i)
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from(wg[i], i), (SV_LDS void *)(stage + S::kTokens * kRowB + (S::kWaves * i + w) * 1024), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)(xs + s * a.x_scale_stride),
+                                         (SV_LDS void *)(stage + (S::kTokens + S::kWRows) * kRowB + w * kWave * 4), 4, 0, 0);
+    };
+
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS char *)lds));
+    const uint32_t lo = ((kg ^ (col >> 1)) & 7) * 16, hi = (((kg + 4) ^ (col >> 1)) & 7) * 16;
+    const uint32_t xrow = base + (wm * XT * 16 + col) * kRowB, wrow = base + (S::kTokens + wn * WT * 16 + col) * kRowB;
+    const uint32_t srow = base + (S::kTokens + S::kWRows) * kRowB + (w * kWave + col) * 4;
+    const uint32_t wat = base + S::kLds + wn * blocks * 4;
+
+    f32x4 acc[WT][XT];
+#pragma unroll
+    for (int i = 0; i < WT; ++i)
+#pragma unroll
+        for (int t = 0; t < XT; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // W's scales are stored
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i)
+        if (i < blocks) issue(i);
+    for (int s = 0; s < blocks; ++s) {
+        const uint32_t st = static_cast<uint32_t>(s % S::kStages * S::kStageB);
+        if (s + S::kStages - 1 <= blocks)
+            wait_loads<(S::kStages - 2) * S::kLoads>();
+        else
+            wait_loads<0>();
+        asm volatile("s_barrier" ::: "memory");  // the stage is there, and the one before it free
+        if (s + S::kStages - 1 < blocks) issue(s + S::kStages - 1);
+        const uint32_t xl0 = xrow + st + lo, xh0 = xrow + st + hi, wl0 = wrow + st + lo, wh0 = wrow + st + hi;
+        float xv[XT], wv;
+        u32x4 xl[XT], xh[XT], wl[2], wh[2];
+        unrolled<0, XT>([&](auto t) {
+            constexpr int T = decltype(t)::value;
+            xv[T] = lds_read_float<T * 64>(srow + st);
+            xl[T] = lds_read<T * 16 * kRowB>(xl0);
+            xh[T] = lds_read<T * 16 * kRowB>(xh0);
+        });
+        wv = lds_read_float<0>(wat + s * 4);
+        wl[0] = lds_read<0>(wl0);
+        wh[0] = lds_read<0>(wh0);
+        float sc[XT];
+        Operand<F32> xf[XT];
+        f32x4 p[2][XT];
+        unrolled<0, WT>([&](auto ii) {
+            constexpr int i = decltype(ii)::value, cur = i & 1;
+            if constexpr (i + 1 < WT) {
+                wl[cur ^ 1] = lds_read<(i + 1) * 16 * kRowB>(wl0);
+                wh[cur ^ 1] = lds_read<(i + 1) * 16 * kRowB>(wh0);
+            }
+            if constexpr (i == 0) {
+                // everything but the two reads just issued
+                arrived<2>(wl[0], wh[0]);
+                arrived<2>(wv);
+#pragma unroll
+                for (int t = 0; t < XT; ++t) {
+                    arrived<2>(xv[t]);
+                    arrived<2>(xl[t], xh[t]);
+                    xf[t].set(xl[t], xh[t]);
+                    sc[t] = xv[t] * wv;
+                }
+            } else if constexpr (i + 1 < WT) {
+                arrived<2>(wl[cur], wh[cur]);
+            } else {
+                arrived<0>(wl[cur], wh[cur]);
+            }
+            Operand<F32> wf;
+            wf.set(wl[cur], wh[cur]);
+#pragma unroll
+            for (int t = 0; t < XT; ++t) p[cur][t] = block_sum(wf, xf[t]);
+            if constexpr (i > 0) {
+#pragma unroll
+                for (int t = 0; t < XT; ++t) acc[i - 1][t] += p[cur ^ 1][t] * sc[t];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+#pragma unroll
+        for (int t = 0; t < XT; ++t) acc[WT - 1][t] += p[(WT - 1) & 1][t] * sc[t];
+    }
+    const bool parts = a.splits > 1;
+    float *part = a.part + static_cast<long long>(split) * a.M * a.N;
+#pragma unroll
+    for (int t = 0; t < XT; ++t) {
+        const int m = m0 + (wm * XT + t) * 16 + col;
+        if (m >= a.M) continue;
+#pragma unroll
+        for (int i = 0; i < WT; ++i) {
+            const int n = n0 + (wn * WT + i) * 16 + 4 * kg;
+            if (parts)
+                store4<true>(part, a.N, m, n, acc[i][t]);
+            else
+                store4<F32>(a.out, a.N, m, n, acc[i][t]);
+        }
+    }
+}
+
+// The parts of K added in order, VEC outputs a lane.
+template <bool F32, int VEC>
+__global__ __launch_bounds__(kBlock) void k_linear_join(LinearArgs a) {
+    const long long all = static_cast<long long>(a.M) * a.N;
+    const long long at = (static_cast<long long>(blockIdx.x) * kBlock + threadIdx.x) * VEC;
+    if (at >= all) return;
+    float v[VEC];
+    auto load = [&](int s, float (&x)[VEC]) {
+        const float *p = a.part + s * all + at;
+        if constexpr (VEC == 4) {
+            const f32x4 y = *reinterpret_cast<const f32x4 *>(p);
+            x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+        } else {
+            x[0] = *p;
+        }
+    };
+    load(0, v);
+    for (int s = 1; s < a.splits; ++s) {
+        float x[VEC];
+        load(s, x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] += x[e];
+    }
+    if constexpr (VEC == 4) {
+        if constexpr (F32)
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = f32x4{v[0], v[1], v[2], v[3]};
+        else
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+        if constexpr (F32)
+            static_cast<float *>(a.out)[at] = v[0];
+        else
+            static_cast<uint16_t *>(a.out)[at] = static_cast<uint16_t>(pack_bf16(v[0], v[0]));
+    }
+}
+
+// bf16 outputs: the largest tile whose accumulators fit beside two tiles' sums.  fp32:
+// widened operands take twice the registers, so half the rows of W.
+using BigShape = Shape<4, 2, 4, 8, 2>;      // 256 x 256
+using BigShapeWide = Shape<4, 2, 4, 4, 3>;  // 256 x 128
+using MidShape = Shape<2, 2, 2, 4, 3>;      // 64 x 128
+
+template <typename S>
+long long tile_groups(int M, int N) {
+    const long long mtiles = (M + S::kTokens - 1) / S::kTokens, ntiles = (N + S::kWRows - 1) / S::kWRows;
+    return mtiles * ((ntiles + kXcds - 1) / kXcds) * kXcds;
+}
+template <typename S, bool F32>
+hipError_t launch_tile(const LinearArgs &a, hipStream_t s) {
+    const int mtiles = (a.M + S::kTokens - 1) / S::kTokens, ntiles = (a.N + S::kWRows - 1) / S::kWRows;
+    const int blocks = (a.K + kScaleBlock - 1) / kScaleBlock;
+    const size_t lds = S::kLds + static_cast<size_t>(S::WN) * ((blocks + a.splits - 1) / a.splits) * 4;
+    const dim3 grid(static_cast<unsigned>(tile_groups<S>(a.M, a.N) * a.splits));
+    return launch_kernel(k_linear_tile<S, F32>, grid, dim3(S::kWaves * kWave), lds, s, a, mtiles, ntiles);
+}
+
+template <int MT, int NT, int WAVES>
+hipError_t launch_few(const LinearArgs &a, bool f32, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>((a.N + 16 * NT - 1) / (16 * NT)), static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)));
+    return f32 ? launch_kernel(k_linear_few<MT, NT, WAVES, true>, grid, dim3(WAVES * kWave), 0, s, a)
+               : launch_kernel(k_linear_few<MT, NT, WAVES, false>, grid, dim3(WAVES * kWave), 0, s, a);
+}
+
+}  // namespace
+
+enum { kFew = 0, kMid = 1, kBig = 2 };
+
+LinearPlan linear_plan(int M, int N, int K, bool f32) {
+    LinearPlan p = {};
+    p.splits = 1;
+    const int blocks = (K + kScaleBlock - 1) / kScaleBlock;
+    if (M <= 64) {
+        p.kind = kFew;
+        p.groups = (N + 15) / 16;
+        return p;
+    }
+    const long long big = f32 ? tile_groups<BigShapeWide>(M, N) : tile_groups<BigShape>(M, N);
+    if (big >= 200) {
+        p.kind = kBig;
+        p.groups = big;
+        return p;
+    }
+    p.kind = kMid;
+    p.groups = tile_groups<MidShape>(M, N);
+    const long long parts = 512 / p.groups;
+    p.splits = static_cast<int>(std::max(1LL, std::min<long long>(parts, blocks / 8)));
+    p.groups *= p.splits;
+    if (p.splits > 1) p.total = static_cast<size_t>(p.splits) * M * N * 4;
+    return p;
+}
+
+hipError_t launch_linear(const LinearArgs &a, const LinearPlan &p, bool f32, hipStream_t s) {
+    if (p.kind == kBig) return f32 ? launch_tile<BigShapeWide, true>(a, s) : launch_tile<BigShape, false>(a, s);
+    if (p.kind == kMid) return f32 ? launch_tile<MidShape, true>(a, s) : launch_tile<MidShape, false>(a, s);
+    const bool wide = a.N >= 16384;
+    if (a.M <= 16) return wide ? launch_few<1, 2, 4>(a, f32, s) : launch_few<1, 1, 4>(a, f32, s);
+    if (a.M <= 32) return wide ? launch_few<2, 2, 4>(a, f32, s) : launch_few<2, 1, 4>(a, f32, s);
+    return wide ? launch_few<4, 2, 4>(a, f32, s) : launch_few<4, 1, 4>(a, f32, s);
+}
+
+hipError_t launch_linear_join(const LinearArgs &a, bool f32, hipStream_t s) {
+    const long long all = static_cast<long long>(a.M) * a.N;
+    const bool four = all % 4 == 0;
+    const long long per = kBlock * (four ? 4 : 1);
+    const dim3 grid(static_cast<unsigned>((all + per - 1) / per));
+    if (four)
+        return f32 ? launch_kernel(k_linear_join<true, 4>, grid, dim3(kBlock), 0, s, a)
+                   : launch_kernel(k_linear_join<false, 4>, grid, dim3(kBlock), 0, s, a);
+    return f32 ? launch_kernel(k_linear_join<true, 1>, grid, dim3(kBlock), 0, s, a)
+               : launch_kernel(k_linear_join<false, 1>, grid, dim3(kBlock), 0, s, a);
+}
+
+}  // namespace sv

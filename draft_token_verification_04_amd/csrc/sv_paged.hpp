@@ -45,4 +45,20 @@ __device__ __forceinline__ int window_rows(const int32_t *__restrict__ counts, i
     return c < 0 ? 0 : (c > N ? N : c);
 }
 
+// The last i in [0, n) with v[i] <= x (v rising), or -1, found by a whole wave 64
+// entries at a time.  Entries that do not rise still give an i in range.
+__device__ __forceinline__ int last_not_above(const int32_t *__restrict__ v, int n, int x, int lane) {
+    int lo = 0, len = n;
+    for (;;) {
+        const int step = (len + kWave - 1) / kWave;
+        const long long i = lane * static_cast<long long>(step);
+        const uint64_t below = __ballot(i < len && v[lo + i] <= x);
+        if (below == 0) return lo - 1;  // only in the first round: v[lo] <= x in the others
+        const int k = 63 - __clzll(static_cast<long long>(below));
+        if (step == 1) return lo + k;
+        lo += k * step;
+        len = min(step, len - k * step);
+    }
+}
+
 }  // namespace sv

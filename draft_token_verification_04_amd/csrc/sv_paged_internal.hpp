@@ -27,6 +27,10 @@ struct AppendArgs {
     void *k_pages, *v_pages;
     float *k_scale, *v_scale;
     int32_t *status;
+    // packed sequences: token t of request b, starts[b] <= t < starts[b + 1]
+    const int32_t *starts;     // [B + 1], or null: windows of N
+    const int32_t *pair_axis;  // [rot / 2] axis of each pair, or null: the first
+    int B, T, axes;            // positions is [axes][T]
 };
 hipError_t launch_append(const AppendArgs &a, int D, bool e4m3, int tokens, hipStream_t s);
 

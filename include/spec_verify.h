@@ -77,7 +77,8 @@ typedef enum {
 typedef enum {
     SV_F32 = 0,
     SV_BF16 = 1,
-    SV_E4M3 = 2, /* 8-bit floats (e4m3, no infinities): elements of a paged cache only */
+    SV_E4M3 = 2, /* 8-bit floats (e4m3, no infinities): elements of a paged cache, and outputs
+                    of spec_rms_norm */
     SV_DTYPE_MIN_ENUM = -0x7fffffff - 1, /* not dtypes: the type spans every int */
     SV_DTYPE_MAX_ENUM = 0x7fffffff
 } sv_dtype;
@@ -497,6 +498,115 @@ sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, 
                               int32_t *top_ids, float *top_logprobs, int32_t *row_status, void *workspace,
                               size_t workspace_bytes, hipStream_t stream);
 
+/* Most columns spec_rms_norm accepts, longest sum of spec_linear_e4m3, and most axes of
+ * the positions spec_append_kv_packed accepts. */
+#define SV_MAX_NORM_COLS 16384
+#define SV_MAX_LINEAR_K 131072
+#define SV_MAX_AXES 4
+
+/*
+ * RMS norm of rows, with the residual's addition (what stands between two layers of
+ * the target, and before its LM head):
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight.
+ *
+ *   x [T] rows of D bf16 values, row t at t * x_stride elements (a multiple of 8).
+ *   residual [T][D] bf16 or NULL (h = x), weight [D] bf16 or NULL (no weight), eps >= 0.
+ *   residual_out [T][D] bf16, optional: h; may be residual itself.
+ *   out [T][D] of dtype out_dt: SV_BF16, or SV_E4M3 with out_scale
+ *     [ceil(D / 128)][T] float32 (NULL for bf16): the values y of 128 columns (fewer in
+ *     the last block) are stored as round(y * (448 / a)) with scale a / 448,
+ *     a = max |y| over them (zeros: scale 0).
+ *   D a multiple of 8, at most SV_MAX_NORM_COLS (else SV_ERR_UNSUPPORTED); everything
+ *   16-byte aligned.  out must not overlap the inputs.
+ * Computed in fp32 from h as added, and rounded once, to nearest even (h^2 included:
+ * |h| up to 1e18).  A row that holds an infinity or NaN has no finite norm: what it
+ * gives is NaN where y is.
+ */
+sv_status spec_rms_norm(const void *x, long long x_stride, const void *residual, const void *weight, float eps, int T,
+                        int D, void *residual_out, void *out, sv_dtype out_dt, float *out_scale, hipStream_t stream);
+
+/*
+ * Matrix product of e4m3 operands with a scale for each block of 128 (a projection of
+ * the target, its LM head among them):
+ *   out[m][n] = sum_k (xs x)[m][k] (ws w)[n][k].
+ *
+ *   x [M] rows of K e4m3 values, row m at m * x_stride bytes (a multiple of 16);
+ *   x_scale: the scale of columns 128 b ... 128 b + 127 of row m at
+ *     b * x_scale_stride + m (as spec_rms_norm writes it, with x_scale_stride = T).
+ *   w [N][K] e4m3, w_scale [ceil(N / 128)][ceil(K / 128)] float32, one for each block of
+ *     128 x 128.
+ *   out [M][N] of dtype out_dt, SV_BF16 or SV_F32.
+ *   K a multiple of 16, at most SV_MAX_LINEAR_K (else SV_ERR_UNSUPPORTED); x, w and out
+ *   16-byte aligned.
+ * Products are summed in fp32 within a block of K, the blocks' scaled sums in fp32; the
+ * order is not specified, but the same for the same sizes.
+ * Workspace: sv_linear_workspace_bytes (0 for invalid or unsupported sizes).
+ */
+size_t sv_linear_workspace_bytes(int M, int N, int K, sv_dtype out_dt);
+
+sv_status spec_linear_e4m3(const void *x, long long x_stride, const float *x_scale, long long x_scale_stride,
+                           const void *w, const float *w_scale, int M, int N, int K, void *out, sv_dtype out_dt,
+                           void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * spec_append_kv_paged for packed sequences (whole prompts of different lengths, or
+ * their next chunks), with positions of several axes.
+ *
+ *   q [T] rows of H heads, k and v [T] rows of kv_heads heads, token t at t * stride
+ *     elements, as for spec_append_kv_paged.
+ *   starts [B + 1] int32, rising: the tokens of request b are starts[b] ...
+ *     starts[b + 1] - 1, none where the two are equal.  Tokens outside every request
+ *     write nothing.  starts that do not rise give unspecified rows (none is read or
+ *     written outside the arrays).
+ *   base [B] int32: the request's cached tokens before these, or NULL (none).  Token
+ *     starts[b] + j takes slot base[b] + j.
+ *   positions [axes][T] int32, 1 <= axes <= SV_MAX_AXES (images and video have positions
+ *     of time, height and width); pair_axis [rot / 2] int32 on the device: the axis
+ *     whose position turns each pair, or NULL (the first; axes must then be 1).
+ *   q_weight, k_weight, eps, rope, rot, max_pos, interleaved, cache, page_table [B][P]
+ *     and the arithmetic: as for spec_append_kv_paged.
+ *   q_out [T][H][head_dim] bf16, contiguous, 16-byte aligned.
+ *   token_status [T] optional: 0 (also outside every request); 1 the slot is outside
+ *     the table, or its page outside the cache; 2 a position is outside [0, max_pos), or
+ *     an entry of pair_axis outside [0, axes).
+ */
+sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, long long q_stride, long long k_stride,
+                                long long v_stride, const void *q_weight, const void *k_weight, float eps,
+                                const float *rope, int rot, int max_pos, int interleaved, const int32_t *positions,
+                                int axes, const int32_t *pair_axis, const int32_t *starts, const int32_t *base, int T,
+                                int B, int H, sv_paged_kv cache, const int32_t *page_table, int P, void *q_out,
+                                int32_t *token_status, hipStream_t stream);
+
+/*
+ * Causal attention of packed sequences over a paged cache that already holds their keys
+ * and values (spec_append_kv_packed): whole prompts, or their next chunks, of any
+ * length.
+ *
+ *   q [T] rows of H heads of head_dim bf16 values, token t at t * q_stride elements; H a
+ *     multiple of kv_heads: query head i reads KV head i / (H / kv_heads).
+ *   starts [B + 1], base [B] or NULL, page_table [B][P]: as for spec_append_kv_packed.
+ *     Token starts[b] + j sees the slots below base[b] + j + 1.
+ *   scale > 0 finite.
+ *   out [T][H][head_dim] bf16 = softmax(scale q k^T) v over the slots seen, 16-byte
+ *     aligned; lse [T][H] float32, optional: the log of the sum of exp(scale q k^T) over
+ *     them.  Rows of tokens outside every request are left as they were.
+ *   req_status [B] optional: 0; 1 a token of the request sees a slot outside the table
+ *     (or base[b] < 0), or a page outside the cache: the rows that see it are 0, their
+ *     lse -inf, the rows before them as without it; 2 the request's bounds in starts are
+ *     malformed (its rows are not written).
+ * Weights enter the second product rounded to bf16; sums and references are fp32.
+ * Scores (scale q.k) must lie within +-1e29 and q.k within fp32.  What a masked slot
+ * holds, infinities and NaN included, reaches no row.
+ * Workspace: sv_attend_packed_workspace_bytes (0 for invalid or unsupported sizes), at
+ * most about 512 MB.
+ */
+size_t sv_attend_packed_workspace_bytes(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size);
+
+sv_status spec_attend_packed(const void *q, long long q_stride, sv_paged_kv cache, const int32_t *page_table, int P,
+                             const int32_t *starts, const int32_t *base, int T, int B, int H, float scale, void *out,
+                             float *lse, int32_t *req_status, void *workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
 /*
  * Measurement aid, not a step of the method: reads the `bytes` bytes at `buf`
  * (device memory, 16-byte aligned, bytes a multiple of 16) once, with the
@@ -558,7 +668,13 @@ typedef enum {
     SV_K_COMMIT_PAGED = 21, /* rows of accepted tree paths moved inside a paged cache */
     SV_K_LOGPROB = 22,      /* row statistics and group maxima per segment */
     SV_K_LOGPROB_MERGE = 23, /* segments joined: log probabilities, entropy, alternatives */
-    SV_K_COUNT = 24
+    SV_K_RMS_NORM = 24,     /* RMS norm with the residual's addition */
+    SV_K_LINEAR = 25,       /* product of e4m3 operands with block scales */
+    SV_K_LINEAR_JOIN = 26,  /* its parts of K joined */
+    SV_K_APPEND_PACKED = 27, /* norms, rotation and paged cache write of packed sequences */
+    SV_K_ATTEND_PACKED = 28, /* causal attention of packed sequences over a paged cache */
+    SV_K_ATTEND_PACKED_JOIN = 29, /* its splits joined */
+    SV_K_COUNT = 30
 } sv_kernel_id;
 
 sv_status sv_trace_begin(int capacity, unsigned kernel_mask);

@@ -1,0 +1,100 @@
+"""GPU tests of spec_linear_e4m3 against the 64-bit oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_04_amd as sv
+from gpu_helpers import dev, note
+from prompt_helpers import LinearCase
+
+pytestmark = pytest.mark.gpu
+DTYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+
+
+# few and many tokens, rows of W and columns that end inside a tile and a block
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64, 65, 130, 257])
+@pytest.mark.parametrize("N,K", [(1, 16), (130, 128), (127, 144), (300, 1040), (256, 2048), (517, 2000)])
+@DTYPES
+def test_sizes(M, N, K, dtype):
+    note(f"linear M={M} N={N} K={K} {dtype}")
+    c = LinearCase(np.random.default_rng(M + N + K), M, N, K, pad=16 * (M % 3))
+    c.check(sv.spec_linear_e4m3(*c.upload(), out_dtype=dtype))
+
+
+# enough outputs for the largest tile, ragged in both directions; long sums that are split
+@pytest.mark.parametrize("M,N,K", [(1000, 13100, 400), (2049, 3333, 128), (600, 20000, 272), (96, 250, 16384),
+                                   (200, 1030, 9008), (3, 40000, 512), (40, 17000, 528)])
+@DTYPES
+def test_shapes_of_each_kernel(M, N, K, dtype):
+    note(f"linear M={M} N={N} K={K} {dtype}")
+    c = LinearCase(np.random.default_rng(N), M, N, K, exact=True)
+    out = sv.spec_linear_e4m3(*c.upload(), out_dtype=dtype)
+    x, xs, w, ws = c.upload()
+    column = torch.arange(K, device=dev()) // 128
+    xd = x.double() * xs.double()[column].t()
+    wd = w.double() * ws.double().repeat_interleave(128, 0)[:N][:, column]
+    want = (xd @ wd.t()).to(torch.float32)  # exact: whole multiples of 1/4 far below 2^22
+    assert torch.equal(out, want.to(dtype))
+
+
+@DTYPES
+def test_long_sums(dtype):
+    note(f"linear long {dtype}")
+    for M in (1, 70, 300):
+        c = LinearCase(np.random.default_rng(M), M, 130, 20000)
+        c.check(sv.spec_linear_e4m3(*c.upload(), out_dtype=dtype))
+    c = LinearCase(np.random.default_rng(5), 5, 20, sv.SV_MAX_LINEAR_K)
+    c.check(sv.spec_linear_e4m3(*c.upload(), out_dtype=dtype))
+    c = LinearCase(np.random.default_rng(6), 66, 20, sv.SV_MAX_LINEAR_K)
+    c.check(sv.spec_linear_e4m3(*c.upload(), out_dtype=dtype))
+
+
+@pytest.mark.parametrize("M", [3, 80, 700])
+@DTYPES
+def test_nan_and_zero_scales_stay_in_their_rows(M, dtype):
+    note(f"linear non-finite M={M} {dtype}")
+    N, K = 300, 272
+    c = LinearCase(np.random.default_rng(M), M, N, K)
+    x, xs, w, ws = c.upload()
+    clean = sv.spec_linear_e4m3(x, xs, w, ws, out_dtype=dtype)
+    x2, w2, xs2 = x.clone(), w.clone(), xs.clone()
+    x2.view(torch.uint8)[1, 271] = 0x7f
+    w2.view(torch.uint8)[299, 5] = 0xff
+    xs2[:, 2] = 0
+    out = sv.spec_linear_e4m3(x2, xs2, w2, ws, out_dtype=dtype)
+    gone = torch.zeros(M, N, dtype=torch.bool, device=dev())
+    gone[1], gone[:, 299] = True, True
+    assert torch.isnan(out[gone]).all()
+    assert (out[2, :299] == 0).all()
+    keep = ~gone
+    keep[2] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
+def test_nothing_is_written_outside_and_repeats_are_equal():
+    note("linear guard")
+    for M, N, K, dtype in ((7, 33, 256, torch.float32), (129, 70, 3008, torch.bfloat16), (600, 12900, 128, torch.bfloat16)):
+        c = LinearCase(np.random.default_rng(M), M, N, K)
+        x, xs, w, ws = c.upload()
+        room = torch.full((M * N + 128,), 5.0, dtype=dtype, device=dev())
+        out = room[64:64 + M * N].view(M, N)
+        first = sv.spec_linear_e4m3(x, xs, w, ws, out=out).clone()
+        assert (room[:64] == 5).all() and (room[64 + M * N:] == 5).all()
+        work = torch.full((sv.linear_workspace_bytes(M, N, K, sv._dtype_code(out)),), 0xff, dtype=torch.uint8, device=dev())
+        assert torch.equal(sv.spec_linear_e4m3(x, xs, w, ws, out_dtype=dtype, workspace=work), first)
+
+
+def test_empty_and_refusals():
+    c = LinearCase(np.random.default_rng(0), 4, 140, 256)
+    x, xs, w, ws = c.upload()
+    assert sv.spec_linear_e4m3(x[:0], xs[:, :0], w, ws).shape == (0, 140)
+    for bad in (dict(x=x.float()), dict(x=x[:, :128]), dict(x_scales=xs[:1]), dict(x_scales=xs.t()), dict(w=w[:, :128]),
+                dict(w_scales=ws[:1]), dict(w_scales=ws.double()), dict(w=w.cpu()), dict(out=torch.zeros(4, 141, device=dev()))):
+        with pytest.raises(ValueError):
+            sv.spec_linear_e4m3(**{**dict(x=x, x_scales=xs, w=w, w_scales=ws), **bad})
+    with pytest.raises(TypeError):
+        sv.spec_linear_e4m3(x, xs, w, ws, out_dtype=torch.float16)
+    x, w = (t[:, :8].contiguous() for t in (x, w))
+    with pytest.raises(sv.SpecVerifyError):
+        sv.spec_linear_e4m3(x, xs[:1].contiguous(), w, ws[:, :1].contiguous())
