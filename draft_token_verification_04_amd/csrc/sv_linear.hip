@@ -15,6 +15,8 @@
 // four outputs of one token, whose scale is one register, beside W's, which is uniform.
 // The order of a lane's 32 values of a block is the same for both operands, so any
 // order will do: lane group g takes the 16-byte chunks g and g + 4.
+#include <math.h>
+
 #include <algorithm>
 
 #include "sv_paged.hpp"
@@ -93,96 +95,9 @@ __device__ __forceinline__ void store4(void *out, int N, int m, int n, const f32
     }
 }
 
-// ---- few tokens: W is streamed once ------------------------------------------------
-
-// A workgroup takes 16 NT rows of W and up to 16 MT tokens; its waves take every
-// WAVES-th block of K, straight from memory into registers with kDepth blocks in
-// flight, and join their sums through LDS.
-template <int MT, int NT, int WAVES, bool F32>
-__global__ __launch_bounds__(WAVES *kWave) void k_linear_few(LinearArgs a) {
-    constexpr int kDepth = NT * MT >= 8 ? 2 : 4;
-    __shared__ f32x4 sums[WAVES][NT * MT][kWave];
-    const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
-    const int col = lane & 15, kg = lane >> 4;
-    const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
-    const int blocks = (a.K + kScaleBlock - 1) / kScaleBlock;
-    const float *ws = a.w_scale + static_cast<long long>(n0 / kScaleBlock) * blocks;
-
-    const uint8_t *wp[NT], *xp[MT];
-    const float *xs[MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) wp[t] = a.w + static_cast<long long>(min(n0 + 16 * t + col, a.N - 1)) * a.K + kg * 16;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int m = min(m0 + 16 * t + col, a.M - 1);
-        xp[t] = a.x + m * a.x_stride + kg * 16;
-        xs[t] = a.x_scale + m;
-    }
-    struct Block {
-        u32x4 w[NT][2], x[MT][2];
-        float xs[MT], ws;
-    };
-    // what lies behind K is zero in both operands
-    auto load = [&](Block &b, int kb) {
-        const long long k = static_cast<long long>(kb) * kScaleBlock;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const bool in = k + kg * 16 + half * 64 < a.K;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                b.w[t][half] = in ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[t] + k + half * 64)) : u32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-                b.x[t][half] = in ? *reinterpret_cast<const u32x4 *>(xp[t] + k + half * 64) : u32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t) b.xs[t] = xs[t][kb * a.x_scale_stride];
-        b.ws = ws[kb];
-    };
-    f32x4 acc[NT][MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0, 0, 0, 0};
-    Block b[kDepth];
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i)
-        if (w + i * WAVES < blocks) load(b[i], w + i * WAVES);
-    for (int kb = w; kb < blocks; kb += kDepth * WAVES) {
-#pragma unroll
-        for (int i = 0; i < kDepth; ++i) {
-            if (kb + i * WAVES >= blocks) break;
-            Operand<F32> wf[NT], xf;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) wf[t].set(b[i].w[t][0], b[i].w[t][1]);
-#pragma unroll
-            for (int u = 0; u < MT; ++u) {
-                xf.set(b[i].x[u][0], b[i].x[u][1]);
-                const float s = b[i].xs[u] * b[i].ws;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t][u] += block_sum(wf[t], xf) * s;
-            }
-            if (kb + (i + kDepth) * WAVES < blocks) load(b[i], kb + (i + kDepth) * WAVES);
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) sums[w][t * MT + u][lane] = acc[t][u];
-    __syncthreads();
-    for (int i = w; i < NT * MT; i += WAVES) {
-        f32x4 v = sums[0][i][lane];
-#pragma unroll
-        for (int j = 1; j < WAVES; ++j) v += sums[j][i][lane];
-        const int m = m0 + (i % MT) * 16 + col;
-        if (m < a.M) store4<F32>(a.out, a.N, m, n0 + (i / MT) * 16 + kg * 4, v);
-    }
-}
-
-// ---- many tokens -------------------------------------------------------------------
-
 constexpr int kRowB = kScaleBlock;  // bytes of a slab's row: one block, one cache line
 constexpr int kXcds = 8;
+constexpr int kPastCaches = 2;      // a load's cache policy: non-temporal
 
 template <int I>
 struct Index {
@@ -225,6 +140,126 @@ __device__ __forceinline__ void arrived(float &a) {
     asm volatile("s_waitcnt lgkmcnt(%1)" : "+v"(a) : "i"(N));
 }
 
+// ---- few tokens ----------------------------------------------------------------------
+
+// A workgroup takes 16 NT rows of W and 16 MT tokens; its waves take every WAVES-th
+// block of K, each through a ring of its own in LDS, kStages - 1 blocks ahead and without
+// barriers, and join their sums at the end.  W is read once, past the caches, in whole
+// cache lines (8 rows of 128 bytes a load): 6.7 TB/s, where loads into the operands'
+// registers, 64 bytes of 16 rows each, reach 4.1.  Workgroups begin at different blocks:
+// rows a power of two apart, all read from the same column, would meet few channels
+// (5.4 TB/s).
+template <int MT, int NT, int WAVES, int STAGES, bool F32>
+__global__ __launch_bounds__(WAVES *kWave) void k_linear_few(LinearArgs a) {
+    constexpr int kLoads = 2 * (MT + NT) + 1;
+    constexpr int kStageB = (MT + NT) * 16 * kRowB + kWave * 4;  // tokens, rows of W, scales
+    static_assert(MT <= 2, "32 tokens' scales leave lanes for W's");
+    __shared__ __align__(1024) char lds[WAVES][STAGES * kStageB];
+    const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
+    const int col = lane & 15, kg = lane >> 4;
+    const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
+    const int blocks = (a.K + kScaleBlock - 1) / kScaleBlock, chunks = a.K / 16;
+    const int steps = (blocks - w + WAVES - 1) / WAVES;  // this wave's blocks: w, w + WAVES, ...
+    const int rot = steps > 0 ? static_cast<int>(blockIdx.x * 5u % static_cast<unsigned>(steps)) : 0;
+
+    const uint8_t *xg[2 * MT], *wg[2 * NT];
+    const int ch[2] = {(lane % 8) ^ ((lane / 16) & 7), (lane % 8) ^ ((4 + lane / 16) & 7)};  // of even and odd loads
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) xg[i] = a.x + min(m0 + 8 * i + lane / 8, a.M - 1) * a.x_stride + ch[i % 2] * 16;
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) wg[i] = a.w + static_cast<long long>(min(n0 + 8 * i + lane / 8, a.N - 1)) * a.K + ch[i % 2] * 16;
+    // lanes 0 .. 31: the tokens' scales, the others: W's
+    const float *sg = lane < 32 ? a.x_scale + min(m0 + lane % (16 * MT), a.M - 1)
+                                : a.w_scale + static_cast<long long>(n0 / kScaleBlock) * blocks;
+    const long long sstep = lane < 32 ? a.x_scale_stride : 1;
+    char *ring = lds[w];
+    auto issue = [&](int s) {
+        char *to = ring + s % STAGES * kStageB;
+        const int kb = (s + rot >= steps ? s + rot - steps : s + rot) * WAVES + w;
+        const bool whole = (kb + 1) * 8 <= chunks;
+        auto from = [&](const uint8_t *p, int c) {  // what lies behind K is zero in both operands
+            if (!whole && kb * 8 + c >= chunks) return reinterpret_cast<const uint8_t *>(&kZeroChunk);
+            return p + kb * kScaleBlock;
+        };
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i)
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from(wg[i], ch[i % 2]), (SV_LDS void *)(to + (2 * MT + i) * 1024), 16, 0, kPastCaches);
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from(xg[i], ch[i % 2]), (SV_LDS void *)(to + i * 1024), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)(sg + kb * sstep), (SV_LDS void *)(to + (MT + NT) * 16 * kRowB), 4, 0, 0);
+    };
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS char *)ring));
+    const uint32_t lo = col * kRowB + ((kg ^ (col >> 1)) & 7) * 16, hi = col * kRowB + (((kg + 4) ^ (col >> 1)) & 7) * 16;
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        if (i < steps) issue(i);
+    for (int s = 0; s < steps; ++s) {
+        if (s + STAGES - 1 <= steps)
+            wait_loads<(STAGES - 2) * kLoads>();
+        else
+            wait_loads<0>();
+        const uint32_t st = base + s % STAGES * kStageB;
+        u32x4 xl[MT], xh[MT], wl[NT], wh[NT];
+        float xv[MT], wv;
+        unrolled<0, MT>([&](auto t) {
+            constexpr int T = decltype(t)::value;
+            xl[T] = lds_read<T * 16 * kRowB>(st + lo);
+            xh[T] = lds_read<T * 16 * kRowB>(st + hi);
+            xv[T] = lds_read_float<(MT + NT) * 16 * kRowB + T * 64>(st + col * 4);
+        });
+        wv = lds_read_float<(MT + NT) * 16 * kRowB + 128>(st);
+        unrolled<0, NT>([&](auto t) {
+            constexpr int T = decltype(t)::value;
+            wl[T] = lds_read<(MT + T) * 16 * kRowB>(st + lo);
+            wh[T] = lds_read<(MT + T) * 16 * kRowB>(st + hi);
+        });
+        arrived<0>(wv);
+        Operand<F32> wf[NT], xf;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            arrived<0>(wl[t], wh[t]);
+            wf[t].set(wl[t], wh[t]);
+        }
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+            arrived<0>(xv[u]);
+            arrived<0>(xl[u], xh[u]);
+        }
+        // the stage read in the last round is free
+        if (s + STAGES - 1 < steps) issue(s + STAGES - 1);
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+            xf.set(xl[u], xh[u]);
+            const float sc = xv[u] * wv;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t][u] += block_sum(wf[t], xf) * sc;
+        }
+    }
+    // the sums meet in the rings, which nothing is loaded into any more
+    __syncthreads();
+    static_assert(MT * NT * 1024 <= STAGES * kStageB, "a wave's sums fit in its ring");
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) reinterpret_cast<f32x4 *>(lds[w])[(t * MT + u) * kWave + lane] = acc[t][u];
+    __syncthreads();
+    for (int i = w; i < NT * MT; i += WAVES) {
+        f32x4 v = reinterpret_cast<const f32x4 *>(lds[0])[i * kWave + lane];
+#pragma unroll
+        for (int j = 1; j < WAVES; ++j) v += reinterpret_cast<const f32x4 *>(lds[j])[i * kWave + lane];
+        const int m = m0 + (i % MT) * 16 + col;
+        if (m < a.M) store4<F32>(a.out, a.N, m, n0 + (i / MT) * 16 + kg * 4, v);
+    }
+}
+
+// ---- many tokens -------------------------------------------------------------------
+
 // The shape of a workgroup: WM x WN waves, each with XT tiles of 16 tokens and WT tiles
 // of 16 rows of W, and STAGES stages of LDS.
 template <int WM_, int WN_, int XT_, int WT_, int STAGES_>
@@ -240,20 +275,79 @@ struct Shape {
     static_assert(WT * 16 <= kScaleBlock && kWRows % kScaleBlock == 0, "a wave's rows share a scale");
 };
 
+// The t-th tile in the order of the walk: groups of kGroupN columns of tiles, in them
+// groups of kGroupM rows, so that the 32 workgroups that an XCD runs at a time (one for
+// each compute unit) read 8 + 4 slabs a block through its L2, not 32 + 1.
+constexpr int kGroupM = 8, kGroupN = 4;
+__device__ __forceinline__ void tile_of(int t, int mtiles, int ntiles, int *mt, int *nt) {
+    const int cg = t / (mtiles * kGroupN), in = t - cg * mtiles * kGroupN;
+    const int gn = min(kGroupN, ntiles - cg * kGroupN);
+    const int mg = in / (kGroupM * gn), at = in - mg * kGroupM * gn;
+    const int gm = min(kGroupM, mtiles - mg * kGroupM);
+    *mt = mg * kGroupM + at % gm;
+    *nt = cg * kGroupN + at / gm;
+}
+
+// Sixteen tokens' outputs of a wave, 16 WT columns from n on: turned in LDS (a wave's own
+// `room`, chunk c of row r at c ^ r), so that they leave as whole rows of 16-byte chunks
+// (8191 x 24576 bf16, 400 MB: 110 us less than as 32-byte pieces of 16 rows).  Rows that
+// do not begin at a multiple of 16 bytes leave value by value.
+template <int WT, bool F32, int XT>
+__device__ __forceinline__ void store_rows(void *out, const LinearArgs &a, int m, int n, const f32x4 (&acc)[WT][XT],
+                                           int t, char *room, int lane) {
+    constexpr int kSize = F32 ? 4 : 2, kChunks = WT * kSize, kRow = kChunks * 16;  // of a row
+    const int col = lane & 15, kg = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < WT; ++i) {
+        const int at = 16 * i + 4 * kg;  // the first of the lane's four columns
+        char *p = room + col * kRow + (((at * kSize / 16) ^ col) & (kChunks - 1)) * 16 + at * kSize % 16;
+        if constexpr (F32)
+            *reinterpret_cast<f32x4 *>(p) = acc[i][t];
+        else
+            *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16(acc[i][t].x, acc[i][t].y), pack_bf16(acc[i][t].z, acc[i][t].w)};
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (static_cast<long long>(a.N) * kSize % 16 == 0) {
+        constexpr int kPer = kWave / kChunks;  // rows a store covers
+        const int c = lane % kChunks;
+#pragma unroll
+        for (int i = 0; i < 16 / kPer; ++i) {
+            const int r = i * kPer + lane / kChunks;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(room + r * kRow + ((c ^ r) & (kChunks - 1)) * 16);
+            if (m + r < a.M && n + c * (16 / kSize) < a.N)
+                *reinterpret_cast<u32x4 *>(static_cast<char *>(out) + (static_cast<long long>(m + r) * a.N + n) * kSize + c * 16) = v;
+        }
+    } else {
+        for (int r = 0; r < 16 && m + r < a.M; ++r) {
+            for (int x = lane; x < WT * 16 && n + x < a.N; x += kWave) {
+                const char *p = room + r * kRow + (((x * kSize / 16) ^ r) & (kChunks - 1)) * 16 + x * kSize % 16;
+                const long long to = static_cast<long long>(m + r) * a.N + n + x;
+                if constexpr (F32)
+                    static_cast<float *>(out)[to] = *reinterpret_cast<const float *>(p);
+                else
+                    static_cast<uint16_t *>(out)[to] = *reinterpret_cast<const uint16_t *>(p);
+            }
+        }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before the next tokens' go there
+}
+
 // A workgroup owns a tile of tokens x rows of W and walks its part of K a block at a
 // time.  Both operands' slabs, and each wave's token scales, go straight from memory to
 // LDS, STAGES - 1 blocks ahead; a slab's row is one cache line, its chunk c stored at
 // c ^ ((r >> 1) & 7), so that the reads of 16 rows meet distinct banks.  The products of
 // one row tile run while the one before enters the accumulators.
-template <typename S, bool F32>
+template <typename S, bool F32, bool STREAM>
 __global__ __launch_bounds__(S::kWaves *kWave) void k_linear_tile(LinearArgs a, int mtiles, int ntiles) {
     constexpr int XT = S::XT, WT = S::WT;
     extern __shared__ __align__(1024) char lds[];  // the stages, then W's scales [WN][blocks]
-    const int bid = blockIdx.x % (mtiles * ((ntiles + kXcds - 1) / kXcds) * kXcds);
-    const int split = blockIdx.x / (mtiles * ((ntiles + kXcds - 1) / kXcds) * kXcds);
-    const int xcd = bid % kXcds, j = bid / kXcds;
-    const int mt = j % mtiles, nt = (j / mtiles) * kXcds + xcd;
-    if (nt >= ntiles) return;
+    // each XCD (consecutive workgroups go to consecutive ones) takes a run of the walk
+    const int tiles = mtiles * ntiles, per = (tiles + kXcds - 1) / kXcds;
+    const int bid = blockIdx.x % (per * kXcds), split = blockIdx.x / (per * kXcds);
+    const int t = bid % kXcds * per + bid / kXcds;
+    if (t >= tiles) return;
+    int mt, nt;
+    tile_of(t, mtiles, ntiles, &mt, &nt);
     const int m0 = mt * S::kTokens, n0 = nt * S::kWRows;
     const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
     const int col = lane & 15, kg = lane >> 4;
@@ -279,20 +373,23 @@ __global__ __launch_bounds__(S::kWaves *kWave) void k_linear_tile(LinearArgs a, 
     for (int i = 0; i < S::kWLoads; ++i)
         wg[i] = a.w + static_cast<long long>(min(n0 + row_of(i), a.N - 1)) * a.K + b0 * kScaleBlock + chunk_of(i) * 16;
     const float *xs = a.x_scale + b0 * a.x_scale_stride + min(m0 + wm * XT * 16 + lane % (XT * 16), a.M - 1);
+    const int rot = STREAM ? nt * 5 % blocks : 0;
+    auto turned = [&](int s) { return s + rot >= blocks ? s + rot - blocks : s + rot; };
     auto issue = [&](int s) {
         char *stage = lds + s % S::kStages * S::kStageB;
-        const bool whole = (b0 + s + 1) * 8 <= chunks;
+        const int kb = turned(s);
+        const bool whole = (b0 + kb + 1) * 8 <= chunks;
         auto from = [&](const uint8_t *p, int i) {  // what lies behind K is zero in both operands
-            if (!whole && (b0 + s) * 8 + chunk_of(i) >= chunks) return reinterpret_cast<const uint8_t *>(&kZeroChunk);
-            return p + s * kScaleBlock;
+            if (!whole && (b0 + kb) * 8 + chunk_of(i) >= chunks) return reinterpret_cast<const uint8_t *>(&kZeroChunk);
+            return p + kb * kScaleBlock;
         };
+#pragma unroll
+        for (int i = 0; i < S::kWLoads; ++i)
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from(wg[i], i), (SV_LDS void *)(stage + S::kTokens * kRowB + (S::kWaves * i + w) * 1024), 16, 0, STREAM ? kPastCaches : 0);
 #pragma unroll
         for (int i = 0; i < S::kXLoads; ++i)
             __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from(xg[i], i), (SV_LDS void *)(stage + (S::kWaves * i + w) * 1024), 16, 0, 0);
-#pragma unroll
-        for (int i = 0; i < S::kWLoads; ++i)
-            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)from(wg[i], i), (SV_LDS void *)(stage + S::kTokens * kRowB + (S::kWaves * i + w) * 1024), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)(xs + s * a.x_scale_stride),
+        __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)(xs + kb * a.x_scale_stride),
                                          (SV_LDS void *)(stage + (S::kTokens + S::kWRows) * kRowB + w * kWave * 4), 4, 0, 0);
     };
 
@@ -328,7 +425,7 @@ __global__ __launch_bounds__(S::kWaves *kWave) void k_linear_tile(LinearArgs a, 
             xl[T] = lds_read<T * 16 * kRowB>(xl0);
             xh[T] = lds_read<T * 16 * kRowB>(xh0);
         });
-        wv = lds_read_float<0>(wat + s * 4);
+        wv = lds_read_float<0>(wat + turned(s) * 4);
         wl[0] = lds_read<0>(wl0);
         wh[0] = lds_read<0>(wh0);
         float sc[XT];
@@ -369,20 +466,16 @@ __global__ __launch_bounds__(S::kWaves *kWave) void k_linear_tile(LinearArgs a, 
 #pragma unroll
         for (int t = 0; t < XT; ++t) acc[WT - 1][t] += p[(WT - 1) & 1][t] * sc[t];
     }
-    const bool parts = a.splits > 1;
-    float *part = a.part + static_cast<long long>(split) * a.M * a.N;
+    asm volatile("s_barrier" ::: "memory");  // every wave is done with the slots
+    char *room = lds + w * (16 * WT * 16 * 4);
+    const int n = n0 + wn * WT * 16;
+    if (a.splits > 1) {
+        float *part = a.part + static_cast<long long>(split) * a.M * a.N;
 #pragma unroll
-    for (int t = 0; t < XT; ++t) {
-        const int m = m0 + (wm * XT + t) * 16 + col;
-        if (m >= a.M) continue;
+        for (int t = 0; t < XT; ++t) store_rows<WT, true>(part, a, m0 + (wm * XT + t) * 16, n, acc, t, room, lane);
+    } else {
 #pragma unroll
-        for (int i = 0; i < WT; ++i) {
-            const int n = n0 + (wn * WT + i) * 16 + 4 * kg;
-            if (parts)
-                store4<true>(part, a.N, m, n, acc[i][t]);
-            else
-                store4<F32>(a.out, a.N, m, n, acc[i][t]);
-        }
+        for (int t = 0; t < XT; ++t) store_rows<WT, F32>(a.out, a, m0 + (wm * XT + t) * 16, n, acc, t, room, lane);
     }
 }
 
@@ -425,65 +518,100 @@ __global__ __launch_bounds__(kBlock) void k_linear_join(LinearArgs a) {
 // bf16 outputs: the largest tile whose accumulators fit beside two tiles' sums.  fp32:
 // widened operands take twice the registers, so half the rows of W.
 using BigShape = Shape<4, 2, 4, 8, 2>;      // 256 x 256
-using BigShapeWide = Shape<4, 2, 4, 4, 3>;  // 256 x 128
-using MidShape = Shape<2, 2, 2, 4, 3>;      // 64 x 128
+using BigShapeWide = Shape<4, 2, 4, 4, 2>;  // 256 x 128
+using MidShape = Shape<4, 2, 2, 4, 2>;      // 128 x 128
+using SmallShape = Shape<2, 2, 2, 4, 2>;    // 64 x 128
+
+size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 template <typename S>
-long long tile_groups(int M, int N) {
-    const long long mtiles = (M + S::kTokens - 1) / S::kTokens, ntiles = (N + S::kWRows - 1) / S::kWRows;
-    return mtiles * ((ntiles + kXcds - 1) / kXcds) * kXcds;
+long long tiles_of(int M, int N) {
+    return static_cast<long long>((M + S::kTokens - 1) / S::kTokens) * ((N + S::kWRows - 1) / S::kWRows);
 }
+long long whole_xcds(long long tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
 template <typename S, bool F32>
 hipError_t launch_tile(const LinearArgs &a, hipStream_t s) {
     const int mtiles = (a.M + S::kTokens - 1) / S::kTokens, ntiles = (a.N + S::kWRows - 1) / S::kWRows;
     const int blocks = (a.K + kScaleBlock - 1) / kScaleBlock;
     const size_t lds = S::kLds + static_cast<size_t>(S::WN) * ((blocks + a.splits - 1) / a.splits) * 4;
-    const dim3 grid(static_cast<unsigned>(tile_groups<S>(a.M, a.N) * a.splits));
-    return launch_kernel(k_linear_tile<S, F32>, grid, dim3(S::kWaves * kWave), lds, s, a, mtiles, ntiles);
+    const dim3 grid(static_cast<unsigned>(whole_xcds(tiles_of<S>(a.M, a.N)) * a.splits));
+    return mtiles == 1 ? launch_kernel(k_linear_tile<S, F32, true>, grid, dim3(S::kWaves * kWave), lds, s, a, mtiles, ntiles)
+                       : launch_kernel(k_linear_tile<S, F32, false>, grid, dim3(S::kWaves * kWave), lds, s, a, mtiles, ntiles);
 }
 
-template <int MT, int NT, int WAVES>
+template <int MT, int NT, int WAVES, int STAGES>
 hipError_t launch_few(const LinearArgs &a, bool f32, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>((a.N + 16 * NT - 1) / (16 * NT)), static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)));
-    return f32 ? launch_kernel(k_linear_few<MT, NT, WAVES, true>, grid, dim3(WAVES * kWave), 0, s, a)
-               : launch_kernel(k_linear_few<MT, NT, WAVES, false>, grid, dim3(WAVES * kWave), 0, s, a);
+    return f32 ? launch_kernel(k_linear_few<MT, NT, WAVES, STAGES, true>, grid, dim3(WAVES * kWave), 0, s, a)
+               : launch_kernel(k_linear_few<MT, NT, WAVES, STAGES, false>, grid, dim3(WAVES * kWave), 0, s, a);
 }
 
 }  // namespace
 
-enum { kFew = 0, kMid = 1, kBig = 2 };
+enum { kFew = 0, kSmall = 1, kMid = 2, kBig = 3 };
+
+// Up to 32 tokens the few-token kernel reads W once and nothing else of size; from 17 on
+// each of its waves reads as many bytes of tokens as of W, so with many rows of W the
+// tiles are faster (32 x 151936 x 4096: 195 and 128 us).
+constexpr int kFewTokens = 32, kFewManyRows = 8192;
+
+// Tiles: the shape and the parts of K with the least estimate of
+//   steps * max(alone, tiles per compute unit * step) + join.
+// `alone` is what a block of 128 takes a single workgroup on its compute unit, `step`
+// what it adds where there are several (us; from 256 x 4096 x 12288 and 8191 x 24576 x
+// 4096, fp32 2048 x 151936 x 4096).  The estimate is within 15% of the measured time at
+// 128 to 8191 tokens.
+struct Cost {
+    int kind;
+    double alone, step;
+    long long tiles;
+};
+constexpr double kCus = 256;
 
 LinearPlan linear_plan(int M, int N, int K, bool f32) {
     LinearPlan p = {};
     p.splits = 1;
     const int blocks = (K + kScaleBlock - 1) / kScaleBlock;
-    if (M <= 64) {
+    if (M <= 16 || (M <= kFewTokens && N <= kFewManyRows)) {
         p.kind = kFew;
         p.groups = (N + 15) / 16;
         return p;
     }
-    const long long big = f32 ? tile_groups<BigShapeWide>(M, N) : tile_groups<BigShape>(M, N);
-    if (big >= 200) {
-        p.kind = kBig;
-        p.groups = big;
-        return p;
+    const Cost costs[3] = {{kSmall, f32 ? 0.82 : 0.58, f32 ? 0.60 : 0.37, tiles_of<SmallShape>(M, N)},
+                           {kMid, f32 ? 1.1 : 0.70, f32 ? 1.15 : 0.61, tiles_of<MidShape>(M, N)},
+                           {kBig, f32 ? 1.9 : 1.85, f32 ? 2.15 : 1.9,
+                            f32 ? tiles_of<BigShapeWide>(M, N) : tiles_of<BigShape>(M, N)}};
+    double best = 0;
+    for (const Cost &c : costs) {
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            const double bytes = (splits + 1.0) * M * N * 4;
+            if (splits > 1 && (blocks / splits < 4 || bytes > 256e6)) break;
+            // the largest tile has its compute unit to itself: whole rounds
+            const double per = c.tiles * splits / kCus, rounds = c.kind == kBig ? ceil(per) : per;
+            const double steps = static_cast<double>((blocks + splits - 1) / splits);
+            const double us = steps * std::max(c.alone, rounds * c.step) + (splits > 1 ? 3.5 + bytes / 5e6 : 0.0);
+            if (best != 0 && us >= best) continue;
+            best = us;
+            p.kind = c.kind;
+            p.splits = splits;
+            p.groups = whole_xcds(c.tiles) * splits * (c.kind == kSmall ? 1 : 2);
+        }
     }
-    p.kind = kMid;
-    p.groups = tile_groups<MidShape>(M, N);
-    const long long parts = 512 / p.groups;
-    p.splits = static_cast<int>(std::max(1LL, std::min<long long>(parts, blocks / 8)));
-    p.groups *= p.splits;
-    if (p.splits > 1) p.total = static_cast<size_t>(p.splits) * M * N * 4;
+    if (p.splits > 1) p.total = align_up(static_cast<size_t>(p.splits) * M * N * 4);
     return p;
 }
 
 hipError_t launch_linear(const LinearArgs &a, const LinearPlan &p, bool f32, hipStream_t s) {
     if (p.kind == kBig) return f32 ? launch_tile<BigShapeWide, true>(a, s) : launch_tile<BigShape, false>(a, s);
     if (p.kind == kMid) return f32 ? launch_tile<MidShape, true>(a, s) : launch_tile<MidShape, false>(a, s);
-    const bool wide = a.N >= 16384;
-    if (a.M <= 16) return wide ? launch_few<1, 2, 4>(a, f32, s) : launch_few<1, 1, 4>(a, f32, s);
-    if (a.M <= 32) return wide ? launch_few<2, 2, 4>(a, f32, s) : launch_few<2, 1, 4>(a, f32, s);
-    return wide ? launch_few<4, 2, 4>(a, f32, s) : launch_few<4, 1, 4>(a, f32, s);
+    if (p.kind == kSmall) return f32 ? launch_tile<SmallShape, true>(a, s) : launch_tile<SmallShape, false>(a, s);
+    // waves for each workgroup such that the launch is one round of the card where it can be
+    // (4096 x 4096: 4 waves 5.3 us, 8 4.9; 6144 x 4096: 6.3 and 8.0), and two row tiles a
+    // wave where there are many rounds (151936 x 4096: one 100 us, two 97; with 16 tokens,
+    // fp32, 122 and 110)
+    if (a.M > 16) return a.N <= 4096 ? launch_few<2, 1, 8, 3>(a, f32, s) : launch_few<2, 1, 4, 4>(a, f32, s);
+    if (a.N <= 4096) return launch_few<1, 1, 8, 3>(a, f32, s);
+    return a.N < 16384 ? launch_few<1, 1, 4, 4>(a, f32, s) : launch_few<1, 2, 2, 6>(a, f32, s);
 }
 
 hipError_t launch_linear_join(const LinearArgs &a, bool f32, hipStream_t s) {

@@ -37,7 +37,7 @@ struct LinearArgs {
 struct LinearPlan {
     int kind;      // which kernel (see sv_linear.hip)
     int splits;    // parts of K, joined by a second launch
-    long long groups;
+    long long groups;  // of 256 work items
     size_t total;  // workspace
 };
 LinearPlan linear_plan(int M, int N, int K, bool f32);
