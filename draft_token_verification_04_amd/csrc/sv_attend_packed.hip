@@ -34,34 +34,20 @@ namespace sv {
 namespace {
 
 #define SV_LDS __attribute__((address_space(3)))
+#define SV_GLOBAL __attribute__((address_space(1)))
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kSlots = 64;         // slots of a tile
+constexpr int kGroupRows = 128;    // rows of a workgroup
 constexpr float kSlack = 8.0f;     // weights may reach 2^kSlack before the reference moves
-// Where a row's reference m (a score q.k) has |m c| < kNear, exponents are one fma
-// against its rounded product; beyond, differences of scores.
-constexpr float kNear = 0x1p20f, kFar = -3e38f;
-constexpr float kNoRef = -3.4028234663852886e38f;  // the reference of a row that has met no score
+// The reference of a row that has met no score.
+constexpr float kNoRef = -3.4028234663852886e38f;
 
-__device__ __forceinline__ float shift_of(float m, float c) {
-#pragma clang fp contract(off)
-    const float x = m * c;
-    return fabsf(x) < kNear ? x : kFar;
-}
-__device__ __forceinline__ float relative(float s, float m, float shift, float c) {
-    return shift != kFar ? fmaf(s, c, -shift) : (s - m) * c;
-}
-// log2 of what turns weights relative to one reference into those of another.
-__device__ __forceinline__ float rebase(float m, float shift, float to, float to_shift, float c) {
-    if (shift == kFar) return relative(m, to, to_shift, c);
-    return to_shift == kFar ? fmaf(-to, c, shift) : shift - to_shift;
-}
+// Natural log of L 2^(m c).
 __device__ __forceinline__ float log_sum(float m, float L, float c) {
-    const float shift = shift_of(m, c);
-    const double x = shift != kFar ? static_cast<double>(shift) : static_cast<double>(m) * static_cast<double>(c);
-    return static_cast<float>((x + static_cast<double>(log2f(L))) * 0.6931471805599453);
+    return static_cast<float>((static_cast<double>(m) * static_cast<double>(c) + static_cast<double>(log2f(L))) * 0.6931471805599453);
 }
 
 // Over the lanes l and l ^ 32 that hold one row.
@@ -94,6 +80,48 @@ __device__ __forceinline__ unsigned finite_only(unsigned w) {
     if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
     return w;
 }
+
+template <int I>
+struct Index {
+    static constexpr int value = I;
+};
+template <int I, int N, typename F>
+__device__ __forceinline__ void unrolled(F &&f) {
+    if constexpr (I < N) {
+        f(Index<I>{});
+        unrolled<I + 1, N>(f);
+    }
+}
+
+// 16 bytes, or a transposed read's 8, at LDS address at + OFF; there once `arrived` has
+// named the register.  (With loads into LDS on their way the compiler would wait for all
+// of them before each LDS read of its own.)
+template <int OFF>
+__device__ __forceinline__ u32x4 lds_read(uint32_t at) {
+    static_assert(OFF >= 0 && OFF < 65536, "ds offset range");
+    u32x4 r;
+    asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(r) : "v"(at), "i"(OFF));
+    return r;
+}
+template <int OFF>
+__device__ __forceinline__ u32x2 lds_read_turned(uint32_t at) {
+    static_assert(OFF >= 0 && OFF < 65536, "ds offset range");
+    u32x2 r;
+    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(r) : "v"(at), "i"(OFF));
+    return r;
+}
+// All but the wave's N youngest LDS reads have arrived, these registers among them.
+template <int N>
+__device__ __forceinline__ void arrived(u32x4 &a) {
+    asm volatile("s_waitcnt lgkmcnt(%1)" : "+v"(a) : "i"(N));
+}
+template <int N>
+__device__ __forceinline__ void arrived(u32x2 &a, u32x2 &b) {
+    asm volatile("s_waitcnt lgkmcnt(%2)" : "+v"(a), "+v"(b) : "i"(N));
+}
+
+// Keeps a value's computation where it is written.
+__device__ __forceinline__ void pin(float &x) { asm volatile("" : "+v"(x)); }
 
 // The row tile a workgroup takes: rows [r0, r0 + rows of a workgroup) of request b.
 struct Unit {
@@ -157,19 +185,17 @@ __device__ __forceinline__ int v_chunk(int r, int c) {
     return D == 64 ? c ^ (2 * (r & 3)) : c ^ (4 * (r & 3)) ^ (2 * ((r >> 1) & 1));
 }
 
-template <int D, bool E4M3, int QT>
-__global__ __launch_bounds__(kBlock, QT * D > 128 ? 1 : 2) void k_attend_packed(PackedArgs a) {
-    constexpr int kRows = 128 * QT;               // of a workgroup
+template <int D, bool E4M3>
+__global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(PackedArgs a) {
+    constexpr int kRows = kGroupRows;             // of a workgroup
     constexpr int kSteps = D / 16;                // of the first product
     constexpr int kVals = D / 32;                 // 32-value blocks of a row of V
     constexpr int kRowB = D * 2;                  // bytes of a row in LDS
     constexpr int kElem = E4M3 ? 1 : 2;
     constexpr int kRowChunks = D * kElem / 16;    // 16-byte chunks of a row in memory
-    constexpr int kLoads = kSlots * kRowChunks / kBlock;  // of a lane, for K and for V
-    constexpr int kStep = kBlock / kRowChunks;    // rows that one load of the workgroup covers
-    __shared__ __align__(1024) char kv[2][2][kSlots * kRowB];  // [stage][K, V]
-    __shared__ __align__(16) float scales[2][2][kSlots];       // e4m3: of the tile's slots
-    __shared__ int odd_tile[2];                   // the tile of a stage where V has a non-finite value
+    __shared__ __align__(1024) char kv[2][2][kSlots * kRowB];  // [K, V][tile's parity]
+    __shared__ __align__(16) float scales[2][2][kSlots];       // e4m3: of the tile's slots, likewise
+    __shared__ int odd_tile[2];                   // first and last tile where V has a non-finite value
     const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
     const int half = lane >> 5, col = lane & 31;
 
@@ -185,8 +211,8 @@ __global__ __launch_bounds__(kBlock, QT * D > 128 ? 1 : 2) void k_attend_packed(
     const Unit un = find_unit(a, u, kRows, lane);
     if (un.b < 0) return;
     const int base = a.base ? uniform(a.base[un.b]) : 0;
-    const int rows = static_cast<int>(min(static_cast<long long>(un.count) * a.G - static_cast<long long>(un.tile) * kRows, static_cast<long long>(kRows)));
     const long long r0 = static_cast<long long>(un.tile) * kRows;
+    const int rows = static_cast<int>(min(static_cast<long long>(un.count) * a.G - r0, static_cast<long long>(kRows)));
     // slots that exist, and the slots that the tile's first and last row see
     const long long exist = static_cast<long long>(a.P) << a.page_shift;
     const long long want = static_cast<long long>(base) + (r0 + rows - 1) / a.G + 1;
@@ -201,301 +227,363 @@ __global__ __launch_bounds__(kBlock, QT * D > 128 ? 1 : 2) void k_attend_packed(
     const int t0 = static_cast<int>(static_cast<long long>(tiles) * split / active);
     const int t1 = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / active);
 
-    // this lane's query rows and how many slots they see
-    bf16x8 q[QT][kSteps];
-    int sees[QT], token[QT], head[QT];
-    int wave_least = 0x7fffffff, wave_most = 0;
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const int r = w * 32 * QT + t * 32 + col;
-        const bool live = r < rows;
-        const long long at = r0 + (live ? r : 0);
-        const int j = static_cast<int>(at / a.G), g = static_cast<int>(at - static_cast<long long>(j) * a.G);
-        token[t] = live ? un.first + j : -1;
-        head[t] = h * a.G + g;
-        sees[t] = live ? static_cast<int>(min(static_cast<long long>(base) + j + 1, exist + 1)) : 0;
-        const uint16_t *p = a.q + (un.first + j) * a.q_stride + static_cast<long long>(head[t]) * D + half * 8;
+    // this lane's query row and how many slots it sees; the wave's least, and the end of
+    // its tiles
+    const int r = w * 32 + col;
+    const bool live = r < rows;
+    const long long at = r0 + (live ? r : 0);
+    const int j = static_cast<int>(at / a.G), head = h * a.G + static_cast<int>(at - static_cast<long long>(j) * a.G);
+    const int token = un.first + j;
+    const int sees = live ? static_cast<int>(min(static_cast<long long>(base) + j + 1, exist + 1)) : 0;
+    bf16x8 q[kSteps];
+    {
+        const uint16_t *p = a.q + token * a.q_stride + static_cast<long long>(head) * D + half * 8;
 #pragma unroll
         for (int c = 0; c < kSteps; ++c) {
             u32x4 x = {0, 0, 0, 0};
             if (live) x = *reinterpret_cast<const u32x4 *>(p + c * 16);
-            q[t][c] = __builtin_bit_cast(bf16x8, x);
+            q[c] = __builtin_bit_cast(bf16x8, x);
         }
     }
+    int wave_least = 0, wave_end = t0;
     {
-        const long long ra = r0 + w * 32 * QT, rb = min(ra + 32 * QT, r0 + rows) - 1;
+        const long long ra = r0 + w * 32, rb = min(ra + 32, r0 + rows) - 1;
         if (rb >= ra) {
             wave_least = static_cast<int>(min(base + ra / a.G + 1, exist + 1));
-            wave_most = static_cast<int>(min(base + rb / a.G + 1, exist + 1));
+            const long long most = min(base + rb / a.G + 1, exist);
+            wave_end = static_cast<int>(min(static_cast<long long>(t1), (most + kSlots - 1) / kSlots));
         }
     }
 
-    f32x16 o[QT][kVals];
-    float m[QT], shift[QT], l[QT];
+    f32x16 o[kVals];
+    float m = kNoRef, l = 0.0f;  // reference (a score q.k), and the weights' sum
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        m[t] = kNoRef;
-        shift[t] = kFar;
-        l[t] = 0.0f;
+    for (int i = 0; i < kVals; ++i)
 #pragma unroll
-        for (int i = 0; i < kVals; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[t][i][e] = 0.0f;
-    }
-    bool far = false;  // a row of the wave has a reference too large for the fma
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
 
-    // ---- a tile's rows, from memory to registers to LDS
+    // ---- rows from memory to LDS: V's stage holds a tile; K's window j, half a tile
+    // earlier, the 64 slots from 64 j - 32 on.  Wave w brings the w-th 16 of them, which
+    // lie in one page; a bf16 cache's straight into LDS, an e4m3 cache's through registers
     const int32_t *table = a.page_table + static_cast<long long>(un.b) * a.P;
     const int page_mask = (1 << a.page_shift) - 1;
-    int ids = 0;  // lane i: the page of the i-th 16 slots of 16 tiles
-    const int row_in = static_cast<int>(threadIdx.x) / kRowChunks, chunk = static_cast<int>(threadIdx.x) % kRowChunks;
-    u32x4 kr[kLoads], vr[kLoads];
-    float sr = 0.0f;
-    auto load = [&](int tile) {
-        const int in = (tile - t0) & 15;
-        if (in == 0) {
-            const int s = tile * kSlots + 16 * lane;
-            const bool there = s < total;
-            ids = there ? table[s >> a.page_shift] : 0;
-            const bool bad = ids < 0 || ids >= a.num_pages;
-            if (bad) {
-                if (s < t1 * kSlots) first_bad = min(first_bad, s);
-                ids = 0;
+    constexpr int kLaneRows = kWave / kRowChunks;  // rows that one load of a wave covers
+    constexpr int kLoads = 16 / kLaneRows;
+    constexpr int kTileB = kSlots * kRowB;
+    const int row_in = lane / kRowChunks, chunk = lane % kRowChunks;
+    struct Stream {
+        int ids, end;  // lane i: the page of 16 slots, the i-th of 64 groups before `end`
+        u32x4 x[E4M3 ? kLoads : 1];
+        float scale;
+    } ks, vs;
+    ks.end = vs.end = -0x7fffffff;
+    auto load = [&](Stream &s, int slot, const void *pages, const float *scale, char *stage, bool is_k) {
+        const int group0 = slot / 16 - t0 * 4;  // in groups of 16 slots from the first tile on
+        if (group0 >= s.end) {
+            s.end = group0 + kWave;
+            const int mine = slot + 16 * lane;
+            s.ids = mine >= 0 && mine < total ? table[mine >> a.page_shift] : 0;
+            if (s.ids < 0 || s.ids >= a.num_pages) {
+                if (mine >= t0 * kSlots && mine < t1 * kSlots) first_bad = min(first_bad, mine);
+                s.ids = 0;
             }
         }
-        auto row_of = [&](int group) {  // the row of the cache where 16 slots of the tile begin
-            const int page = __builtin_amdgcn_readlane(ids, in * 4 + group);
-            const int s = tile * kSlots + 16 * group;
-            return ((static_cast<long long>(page) * a.Hkv + h) << a.page_shift) + (s & page_mask);
-        };
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            // a wave's rows lie in one group of 16 slots
-            const int r = i * kStep + row_in, group = uniform((i * kStep + w * (kStep / 4)) / 16);
-            const long long at = (row_of(group) + (r & 15)) * (D * kElem) + chunk * 16;
-            kr[i] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.k_pages) + at);
-            vr[i] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.v_pages) + at);
-        }
+        const int page = __builtin_amdgcn_readlane(s.ids, group0 + w - (s.end - kWave));
+        const long long row = ((static_cast<long long>(page) * a.Hkv + h) << a.page_shift) + ((slot + 16 * w) & page_mask);
+        const char *from = static_cast<const char *>(pages) + row * (D * kElem);
         if constexpr (E4M3) {
-            // waves 0 and 1: lane i the scale of slot i, of K and of V
-            if (w < 2) {
-                long long at = 0;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const long long x = row_of(g) + (lane & 15);
-                    if (lane / 16 == g) at = x;
-                }
-                sr = (w == 0 ? a.k_scale : a.v_scale)[at];
+            for (int i = 0; i < kLoads; ++i) s.x[i] = *reinterpret_cast<const u32x4 *>(from + (i * kLaneRows + row_in) * (D * kElem) + chunk * 16);
+            s.scale = scale[row + (lane & 15)];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = i * kLaneRows + row_in;  // place `chunk` of the row holds chunk
+                const int c = is_k ? k_chunk<D>(r, chunk) : v_chunk<D>(r, chunk);
+                __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)(from + r * kRowB + c * 16),
+                                                 (SV_LDS void *)(stage + w * 16 * kRowB + i * 1024), 16, 0, 0);
             }
         }
     };
-    auto store = [&](int tile) {
-        const int st = (tile - t0) & 1;
-        const bool edge = (tile + 1) * kSlots > least;  // some row does not see all of it
-        bool odd = false;
+    auto load_k = [&](int window) {
+        load(ks, window * kSlots - kSlots / 2, a.k_pages, a.k_scale, kv[0][(window - t0) & 1], true);
+    };
+    auto load_v = [&](int tile) { load(vs, tile * kSlots, a.v_pages, a.v_scale, kv[1][(tile - t0) & 1], false); };
+    auto store = [&](Stream &s, char *stage, float *scale, bool is_k) {  // e4m3: widened
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = i * kStep + row_in;
-            constexpr int kParts = E4M3 ? 2 : 1;
-            u32x4 kp[kParts], vp[kParts];
-            if constexpr (E4M3) {
+        for (int i = 0; i < (E4M3 ? kLoads : 0); ++i) {
+            const int r = 16 * w + i * kLaneRows + row_in;
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < 2; ++p) {
+                u32x4 y;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        kp[p][2 * e] = e4m3_to_bf16<false>(kr[i][2 * p + e]);
-                        kp[p][2 * e + 1] = e4m3_to_bf16<true>(kr[i][2 * p + e]);
-                        vp[p][2 * e] = e4m3_to_bf16<false>(vr[i][2 * p + e]);
-                        vp[p][2 * e + 1] = e4m3_to_bf16<true>(vr[i][2 * p + e]);
-                    }
-            } else {
-                kp[0] = kr[i];
-                vp[0] = vr[i];
-            }
-            if (edge) {
-                const bool behind = tile * kSlots + r >= total;
-#pragma unroll
-                for (int p = 0; p < kParts; ++p)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (behind) vp[p][e] = 0;
-                        odd |= has_nonfinite(vp[p][e]);
-                        vp[p][e] = finite_only(vp[p][e]);
-                    }
-            }
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-                const int c = chunk * kParts + p;
-                *reinterpret_cast<u32x4 *>(&kv[st][0][r * kRowB + k_chunk<D>(r, c) * 16]) = kp[p];
-                *reinterpret_cast<u32x4 *>(&kv[st][1][r * kRowB + v_chunk<D>(r, c) * 16]) = vp[p];
+                for (int e = 0; e < 2; ++e) {
+                    y[2 * e] = e4m3_to_bf16<false>(s.x[i][2 * p + e]);
+                    y[2 * e + 1] = e4m3_to_bf16<true>(s.x[i][2 * p + e]);
+                }
+                const int c = is_k ? k_chunk<D>(r, chunk * 2 + p) : v_chunk<D>(r, chunk * 2 + p);
+                *reinterpret_cast<u32x4 *>(stage + r * kRowB + c * 16) = y;
             }
         }
-        if (odd) odd_tile[st] = tile;
-        if constexpr (E4M3) {
-            if (w < 2) scales[st][w][lane] = sr;
+        if (lane < 16) scale[16 * w + lane] = s.scale;
+    };
+    auto store_k = [&](int window) {
+        if constexpr (E4M3) store(ks, kv[0][(window - t0) & 1], scales[0][(window - t0) & 1], true);
+    };
+    auto store_v = [&](int tile) {
+        if constexpr (E4M3) store(vs, kv[1][(tile - t0) & 1], scales[1][(tile - t0) & 1], false);
+    };
+    // A tile's values that some row does not see: those behind the last slot zeroed, and
+    // what is not finite left out (and noted)
+    auto clean_v = [&](int tile) {
+        char *stage = kv[1][(tile - t0) & 1];
+        bool odd = false;
+        for (int i = threadIdx.x; i < kTileB / 16; i += kBlock) {
+            u32x4 y = *reinterpret_cast<u32x4 *>(stage + i * 16);
+            const bool behind = tile * kSlots + i / (kRowB / 16) >= total;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (behind) y[e] = 0;
+                odd |= has_nonfinite(y[e]);
+                y[e] = finite_only(y[e]);
+            }
+            *reinterpret_cast<u32x4 *>(stage + i * 16) = y;
+        }
+        if (odd) {
+            atomicMin(&odd_tile[0], tile);
+            atomicMax(&odd_tile[1], tile);
         }
     };
 
-    if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
+    // ---- the parts of a half tile's work; slot 64 tile + 32 f + 8 (e / 4) + 4 half + e % 4
+    // of row col is score s[e] of half f
+    uint32_t kp[kSteps], vp[kVals];  // LDS addresses in the stage of even windows and tiles
+    const uint32_t k0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS char *)&kv[0][0][0]));
+    const uint32_t v0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS char *)&kv[1][0][0]));
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) kp[c] = k0 + col * kRowB + k_chunk<D>(col, 2 * c + half) * 16;
+#pragma unroll
+    for (int d = 0; d < kVals; ++d) {
+        // lane i of 16 addresses 4 values of row i / 4 and gets value i of the 4 rows
+        const int r = 4 * half + (lane & 15) / 4, byte = (d * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
+        vp[d] = v0 + r * kRowB + v_chunk<D>(r, byte / 16) * 16 + byte % 16;
+    }
+    const SV_LDS f32x4 *kscale = (const SV_LDS f32x4 *)&scales[0][0][0] + half, *vscale = (const SV_LDS f32x4 *)&scales[1][0][0] + half;
+    auto k_part = [&](auto par, auto f, auto c) {
+        return lds_read<decltype(f)::value * 32 * kRowB + decltype(par)::value * kTileB>(kp[decltype(c)::value]);
+    };
+    struct Turned {
+        u32x2 lo, hi;
+    };
+    auto v_part = [&](auto par, auto f, auto i) {
+        constexpr int g = decltype(i)::value / kVals, d = decltype(i)::value % kVals;
+        constexpr int kOff = (decltype(f)::value * 32 + g * 16) * kRowB + decltype(par)::value * kTileB;
+        Turned t;
+        t.lo = lds_read_turned<kOff>(vp[d]);
+        t.hi = lds_read_turned<kOff + 8 * kRowB>(vp[d]);
+        return t;
+    };
+    constexpr int kMixes = 2 * kVals, kAhead = kSteps < 4 ? kSteps - 1 : 3;  // fragments on their way
+    // minus the reference, and as what a bf16 cache's sums begin at
+    float minus_m = 0.0f;
+    f32x16 minus;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) minus[e] = 0.0f;
+    // A half's weights out of its scores (relative to the reference), and the next half's
+    // products, a product to a few weights.  The sums of a bf16 cache begin at minus the
+    // reference: what leaves them is already relative to it.
+    auto weigh = [&](auto par, auto f, int tile, f32x16 &s, f32x16 &next, bf16x8 (&p)[2]) {
+        constexpr int F = decltype(f)::value, kWindow = 1 - decltype(par)::value;
+        const int seen = sees - tile * kSlots - 4 * half;
+        u32x4 kf[kAhead + 1];
+        unrolled<0, kAhead>([&](auto c) { kf[decltype(c)::value] = k_part(Index<kWindow>{}, f, c); });
+        float sum[2] = {0, 0};
+        f32x4 vs4;
+        unrolled<0, kSteps>([&](auto cc) {
+            constexpr int c = decltype(cc)::value, kPer = 16 / kSteps;
+            if constexpr (c + kAhead < kSteps) kf[(c + kAhead) % (kAhead + 1)] = k_part(Index<kWindow>{}, f, Index<c + kAhead>{});
+            arrived<(kSteps - 1 - c < kAhead ? kSteps - 1 - c : kAhead)>(kf[c % (kAhead + 1)]);
+            next = mfma32(__builtin_bit_cast(bf16x8, kf[c % (kAhead + 1)]), q[c], c == 0 ? minus : next);
+            unrolled<0, kPer>([&](auto xx) {
+                constexpr int e = c * kPer + decltype(xx)::value;
+                if constexpr (E4M3 && e % 4 == 0) vs4 = vscale[decltype(par)::value * (kSlots / 4) + 8 * F + 2 * (e / 4)];
+                float y = fast_exp2(s[e] * a.c);
+                sum[e % 2] += y;
+                // a masked slot's scale may be anything
+                if constexpr (E4M3) y = 32 * F + 8 * (e / 4) + e % 4 >= seen ? 0.0f : y * vs4[e % 4];
+                s[e] = y;
+                if constexpr (e % 8 == 7)
+                    p[e / 8] = as_bf16x8(pack_bf16(s[e - 7], s[e - 6]), pack_bf16(s[e - 5], s[e - 4]), pack_bf16(s[e - 3], s[e - 2]),
+                                         pack_bf16(s[e - 1], s[e]));
+            });
+            pin(sum[0]);
+            pin(sum[1]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        l += sum[0] + sum[1];
+    };
+    // The half's values mixed, and the next half's largest score (an e4m3 cache's scores
+    // scaled and made relative first)
+    auto mix = [&](auto par, auto f, const bf16x8 (&p)[2], f32x16 &next) {
+        constexpr int F = decltype(f)::value, kWindow = 1 - decltype(par)::value;
+        Turned vf[kAhead + 1];
+        unrolled<0, kAhead>([&](auto i) { vf[decltype(i)::value] = v_part(par, f, i); });
+        float most = -__builtin_huge_valf();
+        f32x4 ks4;
+        unrolled<0, kMixes>([&](auto ii) {
+            constexpr int i = decltype(ii)::value, g = i / kVals, d = i % kVals;
+            if constexpr (i + kAhead < kMixes) vf[(i + kAhead) % (kAhead + 1)] = v_part(par, f, Index<i + kAhead>{});
+            Turned &v = vf[i % (kAhead + 1)];
+            arrived<2 * (kMixes - 1 - i < kAhead ? kMixes - 1 - i : kAhead)>(v.lo, v.hi);
+            o[d] = mfma32(as_bf16x8(v.lo.x, v.lo.y, v.hi.x, v.hi.y), p[g], o[d]);
+            if constexpr (i >= kVals) {  // the scores are there by now
+                constexpr int kPairs = 8 / kVals;
+                unrolled<0, kPairs>([&](auto xx) {
+                    constexpr int e = ((i - kVals) * kPairs + decltype(xx)::value) * 2;
+                    if constexpr (E4M3) {
+                        if constexpr (e % 4 == 0) ks4 = kscale[kWindow * (kSlots / 4) + 8 * F + 2 * (e / 4)];
+                        next[e] = fmaf(next[e], ks4[e % 4], minus_m);
+                        next[e + 1] = fmaf(next[e + 1], ks4[e % 4 + 1], minus_m);
+                    }
+                    most = fmaxf(most, fmaxf(next[e], next[e + 1]));
+                });
+                pin(most);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        return most;
+    };
+    // Masks the scores from slot `slot` on; the largest then
+    auto masked = [&](int slot, f32x16 &s) {
+        float most = -__builtin_huge_valf();
+        const int seen = sees - slot - 4 * half;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            if (8 * (e / 4) + e % 4 >= seen) s[e] = -__builtin_huge_valf();
+            most = fmaxf(most, s[e]);
+        }
+        return most;
+    };
+    // Moves the references where a score is far above its own, and to a row's first score
+    auto refer = [&](float most, f32x16 &s) {
+        const bool moves = m == kNoRef ? most > -__builtin_huge_valf() : most * a.c > kSlack;
+        if (__ballot(moves) == 0) return;
+        const float up = pair_max(most);
+        const bool first = m == kNoRef;
+        const float by = first ? (up > -__builtin_huge_valf() ? up : 0.0f) : fmaxf(up, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] -= by;
+        const float f = first ? 1.0f : fast_exp2(-by * a.c);  // a first reference has nothing to turn
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) o[i] *= f;
+        m = first ? (up > -__builtin_huge_valf() ? up : kNoRef) : m + by;
+        minus_m = m == kNoRef ? 0.0f : -m;
+        if constexpr (!E4M3) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) minus[e] = minus_m;
+        }
+    };
+
+    if (threadIdx.x < 2) odd_tile[threadIdx.x] = threadIdx.x == 0 ? 0x7fffffff : -1;
     __syncthreads();
     if (t0 < t1) {
-        load(t0);
-        store(t0);
+        load_k(t0);
+        load_v(t0);
+        store_k(t0);
+        store_v(t0);
+        load_k(t0 + 1);
+        store_k(t0 + 1);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    for (int tile = t0; tile < t1; ++tile) {
-        __syncthreads();  // the tile is there, and the other stage free
-        const bool more = tile + 1 < t1;
-        if (more) load(tile + 1);
-        const int st = (tile - t0) & 1, s0 = tile * kSlots;
-        if (s0 < wave_most) {
-            // scores: slot s0 + 32 f + 8 (e / 4) + 4 half + e % 4 of row col
-            f32x16 s[QT][2];
+    __syncthreads();
+    // Half tiles, one after the other: the weights of one come out of its scores while the
+    // next one's are formed (behind the wave's last half, scores that nothing reads), then
+    // its values are mixed.
+    f32x16 s, next;
+    float most = 0.0f;
+    if (t0 < wave_end) {
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
+        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+        unrolled<0, kSteps>([&](auto c) {
+            u32x4 x = k_part(Index<0>{}, Index<1>{}, c);
+            arrived<0>(x);
+            s = mfma32(__builtin_bit_cast(bf16x8, x), q[decltype(c)::value], s);
+        });
+        if constexpr (E4M3) {
 #pragma unroll
-                for (int t = 0; t < QT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[t][f][e] = 0.0f;
-#pragma unroll
-                for (int c = 0; c < kSteps; ++c) {
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(
-                        &kv[st][0][(32 * f + col) * kRowB + k_chunk<D>(32 * f + col, 2 * c + half) * 16]);
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) s[t][f] = mfma32(kf, q[t][c], s[t][f]);
-                }
-            }
-            if constexpr (E4M3) {
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&scales[st][0][32 * f + 8 * x + 4 * half]);
-#pragma unroll
-                        for (int t = 0; t < QT; ++t)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[t][f][4 * x + e] *= ks[e];
-                    }
-            }
-            const bool edge = s0 + kSlots > wave_least;
-            if (edge) {
-#pragma unroll
-                for (int t = 0; t < QT; ++t)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int slot = s0 + 32 * f + 8 * (e / 4) + 4 * half + e % 4;
-                            if (slot >= sees[t]) s[t][f][e] = -__builtin_huge_valf();
-                        }
-            }
-            bf16x8 p[QT][4];
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                float most = fmaxf(s[t][0][0], s[t][1][0]);
-#pragma unroll
-                for (int e = 1; e < 16; ++e) most = fmaxf(most, fmaxf(s[t][0][e], s[t][1][e]));
-                const float top = relative(most, m[t], shift[t], a.c);
-                if (__ballot(top > kSlack) != 0) {
-                    const float to = fmaxf(m[t], pair_max(most)), now = shift_of(to, a.c);
-                    const float f = fast_exp2(rebase(m[t], shift[t], to, now, a.c));
-                    l[t] *= f;
-#pragma unroll
-                    for (int i = 0; i < kVals; ++i) o[t][i] *= f;
-                    m[t] = to;
-                    shift[t] = now;
-                    far = false;
-#pragma unroll
-                    for (int x = 0; x < QT; ++x) far |= shift[x] == kFar && m[x] != kNoRef;
-                    far = __ballot(far) != 0;
-                }
-                float sum = 0.0f;
-                if (!far) {
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) s[t][f][e] = fast_exp2(fmaf(s[t][f][e], a.c, -shift[t]));
-                } else {
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) s[t][f][e] = fast_exp2(relative(s[t][f][e], m[t], shift[t], a.c));
-                }
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) sum += s[t][f][e];
-                l[t] += sum;
-                if constexpr (E4M3) {
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const f32x4 vs = *reinterpret_cast<const f32x4 *>(&scales[st][1][32 * f + 8 * x + 4 * half]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int slot = s0 + 32 * f + 8 * x + 4 * half + e;
-                                const float y = s[t][f][4 * x + e] * vs[e];
-                                s[t][f][4 * x + e] = edge && slot >= sees[t] ? 0.0f : y;
-                            }
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int f = i / 2, e = 8 * (i % 2);
-                    p[t][i] = as_bf16x8(pack_bf16(s[t][f][e], s[t][f][e + 1]), pack_bf16(s[t][f][e + 2], s[t][f][e + 3]),
-                                        pack_bf16(s[t][f][e + 4], s[t][f][e + 5]), pack_bf16(s[t][f][e + 6], s[t][f][e + 7]));
-                }
-            }
-            // lane i of 16 addresses 4 values of row i / 4 and gets value i of the 4 rows
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int d = 0; d < kVals; ++d) {
-                    bf16x4 part[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int r = 16 * i + 8 * x + 4 * half + (lane & 15) / 4;
-                        const int byte = (d * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
-                        part[x] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-                            (SV_LDS bf16x4 *)&kv[st][1][r * kRowB + v_chunk<D>(r, byte / 16) * 16 + byte % 16]);
-                    }
-                    const bf16x8 vt = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) o[t][d] = mfma32(vt, p[t][i], o[t][d]);
-                }
-            if (uniform(odd_tile[st]) == tile) {
-                // the non-finite values, one by one, for the rows that see their slot
-                for (int e = 0; e < kSlots && s0 + e < total; ++e) {
-                    const int page = uniform(table[(s0 + e) >> a.page_shift]);
-                    const long long at = (((page < 0 || page >= a.num_pages ? 0LL : page) * a.Hkv + h) << a.page_shift) +
-                                         ((s0 + e) & page_mask);
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) {
-                        float mine = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                if (16 * i + 8 * (x / 4) + 4 * half + x % 4 == e) mine = static_cast<float>(p[t][i][x]);
-                        const float weight = __shfl(mine, ((e >> 2) & 1) * 32 + col, kWave);
-                        if (s0 + e >= sees[t]) continue;
-#pragma unroll
-                        for (int d = 0; d < kVals; ++d)
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const long long i = at * D + d * 32 + 8 * (x / 4) + 4 * half + x % 4;
-                                float v;
-                                if constexpr (E4M3)
-                                    v = __uint_as_float(e4m3_to_bf16<false>(static_cast<const uint8_t *>(a.v_pages)[i]) << 16);
-                                else
-                                    v = bf16_to_f32(static_cast<const uint16_t *>(a.v_pages)[i]);
-                                if (!isfinite(v)) o[t][d][x] += weight * v;
-                            }
-                    }
-                }
-            }
+            for (int e = 0; e < 16; ++e) s[e] *= kscale[8 + 2 * (e / 4)][e % 4];
         }
-        if (more) store(tile + 1);
+        most = masked(t0 * kSlots, s);
+    }
+    auto turn = [&](auto par, int tile) {
+        // the next window of K and this tile's V are there; every wave is done with the ones
+        // before
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __syncthreads();
+        if ((tile + 1) * kSlots > least) {
+            clean_v(tile);
+            __syncthreads();
+        }
+        const bool more = tile + 1 < t1;
+        if (more) {
+            load_k(tile + 2);
+            load_v(tile + 1);
+        }
+        if (tile < wave_end) {
+            bf16x8 p[2];
+            refer(most, s);
+            weigh(par, Index<0>{}, tile, s, next, p);
+            most = mix(par, Index<0>{}, p, next);
+            if ((tile + 1) * kSlots > wave_least) most = masked(tile * kSlots + 32, next);
+            refer(most, next);
+            weigh(par, Index<1>{}, tile, next, s, p);
+            most = mix(par, Index<1>{}, p, s);
+            if ((tile + 2) * kSlots > wave_least) most = masked((tile + 1) * kSlots, s);
+        }
+        if (more) {
+            store_k(tile + 2);
+            store_v(tile + 1);
+        }
+    };
+    int tile = t0;
+    for (; tile + 1 < t1; tile += 2) {
+        turn(Index<0>{}, tile);
+        turn(Index<1>{}, tile + 1);
+    }
+    if (tile < t1) turn(Index<0>{}, tile);
+
+    __syncthreads();
+    if (odd_tile[0] <= odd_tile[1]) {
+        // the non-finite values of V, one by one, for the rows that see their slot
+        const int s1 = min((odd_tile[1] + 1) * kSlots, total);
+        for (int slot = odd_tile[0] * kSlots; slot < s1; ++slot) {
+            const int page = uniform(table[slot >> a.page_shift]);
+            const long long row = (((page < 0 || page >= a.num_pages ? 0LL : page) * a.Hkv + h) << a.page_shift) + (slot & page_mask);
+            auto value = [&](const void *pages, int d) {
+                if constexpr (E4M3)
+                    return __uint_as_float(e4m3_to_bf16<false>(static_cast<const uint8_t *>(pages)[row * D + d]) << 16);
+                else
+                    return bf16_to_f32(static_cast<const uint16_t *>(pages)[row * D + d]);
+            };
+            float score = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) score += static_cast<float>(q[c][e]) * value(a.k_pages, 16 * c + 8 * half + e);
+            score = pair_sum(score);
+            if constexpr (E4M3) score *= a.k_scale[row];
+            if (slot >= sees) continue;
+            float weight = fast_exp2((score - m) * a.c);
+            if constexpr (E4M3) weight *= a.v_scale[row];
+#pragma unroll
+            for (int d = 0; d < kVals; ++d)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float v = value(a.v_pages, d * 32 + 8 * (x / 4) + 4 * half + x % 4);
+                    if (!isfinite(v)) o[d][x] += weight * v;
+                }
+        }
     }
 
     // the first slot of a bad page that the workgroup met
@@ -510,39 +598,35 @@ __global__ __launch_bounds__(kBlock, QT * D > 128 ? 1 : 2) void k_attend_packed(
             a.part_bad[unit] = first_bad;
         }
     }
+    const float L = pair_sum(l);
+    if (!live) return;
+    if (alone) {
+        const bool none = first_bad < sees;
+        const float f = none ? 0.0f : 1.0f / L;
+        const long long to = static_cast<long long>(token) * a.H + head;
+        if (a.lse && half == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m, L, a.c);
+        uint16_t *dst = a.out + to * D + 4 * half;
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const float L = pair_sum(l[t]);
-        if (token[t] < 0) continue;
-        if (alone) {
-            const bool none = first_bad < sees[t];
-            const float f = none ? 0.0f : 1.0f / L;
-            const long long to = static_cast<long long>(token[t]) * a.H + head[t];
-            if (a.lse && half == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m[t], L, a.c);
-            uint16_t *dst = a.out + to * D + 4 * half;
+        for (int d = 0; d < kVals; ++d)
 #pragma unroll
-            for (int d = 0; d < kVals; ++d)
+            for (int x = 0; x < 4; ++x) {
+                float v[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : o[t][d][4 * x + e] * f;
-                    *reinterpret_cast<u32x2 *>(dst + d * 32 + 8 * x) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                }
-        } else {
-            const long long row = unit * kRows + w * 32 * QT + t * 32 + col;
-            if (half == 0) {
-                a.part_ml[row * 2] = m[t];
-                a.part_ml[row * 2 + 1] = L;
+                for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : o[d][4 * x + e] * f;
+                *reinterpret_cast<u32x2 *>(dst + d * 32 + 8 * x) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
             }
-            float *dst = a.part_o + row * D + 4 * half;
-#pragma unroll
-            for (int d = 0; d < kVals; ++d)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    *reinterpret_cast<f32x4 *>(dst + d * 32 + 8 * x) =
-                        f32x4{o[t][d][4 * x], o[t][d][4 * x + 1], o[t][d][4 * x + 2], o[t][d][4 * x + 3]};
+    } else {
+        const long long row = unit * kRows + r;
+        if (half == 0) {
+            a.part_ml[row * 2] = m;
+            a.part_ml[row * 2 + 1] = L;
         }
+        float *dst = a.part_o + row * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < kVals; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<f32x4 *>(dst + d * 32 + 8 * x) = f32x4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]};
     }
 }
 
@@ -573,13 +657,12 @@ __global__ __launch_bounds__(kBlock) void k_packed_join(PackedArgs a, int rows_p
     const int j = static_cast<int>((r0 + r) / a.G), g = static_cast<int>(r0 + r - static_cast<long long>(j) * a.G);
     float m = kNoRef;
     for (int s = 0; s < active; ++s) m = fmaxf(m, a.part_ml[((unit + s) * rows_per + r) * 2]);
-    const float shift = shift_of(m, a.c);
     float L = 0.0f;
     f32x4 o = {0, 0, 0, 0};
     for (int s = 0; s < active; ++s) {
         const long long row = (unit + s) * rows_per + r;
         const float ms = a.part_ml[row * 2], ls = a.part_ml[row * 2 + 1];
-        const float f = ls == 0.0f ? 0.0f : fast_exp2(rebase(ms, shift_of(ms, a.c), m, shift, a.c));
+        const float f = ms == kNoRef ? 0.0f : fast_exp2((ms - m) * a.c);
         L += ls * f;
         o += *reinterpret_cast<const f32x4 *>(a.part_o + row * D + d) * f;
     }
@@ -593,16 +676,11 @@ __global__ __launch_bounds__(kBlock) void k_packed_join(PackedArgs a, int rows_p
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-template <int D, bool E4M3>
-hipError_t launch_qt(const PackedArgs &a, const PackedPlan &p, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(packed_groups(a.Hkv, p)));
-    if constexpr (D < 256)
-        if (p.QT == 2) return launch_kernel(k_attend_packed<D, E4M3, 2>, grid, dim3(kBlock), 0, s, a);
-    return launch_kernel(k_attend_packed<D, E4M3, 1>, grid, dim3(kBlock), 0, s, a);
-}
 template <int D>
 hipError_t launch_d(const PackedArgs &a, bool e4m3, const PackedPlan &p, hipStream_t s) {
-    return e4m3 ? launch_qt<D, true>(a, p, s) : launch_qt<D, false>(a, p, s);
+    const dim3 grid(static_cast<unsigned>(packed_groups(a.Hkv, p)));
+    return e4m3 ? launch_kernel(k_attend_packed<D, true>, grid, dim3(kBlock), 0, s, a)
+                : launch_kernel(k_attend_packed<D, false>, grid, dim3(kBlock), 0, s, a);
 }
 
 }  // namespace
@@ -616,8 +694,7 @@ long long packed_join_groups(int Hkv, int D, const PackedPlan &p) {
 PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size) {
     PackedPlan p = {};
     const long long all = static_cast<long long>(T) * (H / Hkv);
-    p.QT = 1;
-    p.rows = 128 * p.QT;
+    p.rows = kGroupRows;
     // every request may end in a part of a tile; none has more tiles than rows
     p.units = static_cast<int>(std::max(1LL, std::min(all / p.rows + B, all)));
     const long long tiles = (static_cast<long long>(P) * page_size + kSlots - 1) / kSlots;

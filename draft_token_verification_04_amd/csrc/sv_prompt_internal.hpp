@@ -60,7 +60,7 @@ struct PackedArgs {
     int32_t *part_bad;        // [units][Hkv][S]
 };
 struct PackedPlan {
-    int QT, rows;       // 32-row tiles per wave, rows of a workgroup
+    int rows;           // rows of a workgroup
     int units, S;
     size_t part_o, part_ml, part_bad, total;
 };
