@@ -143,7 +143,7 @@ def load_library(path: str = LIB_PATH):
     lib.spec_linear_e4m3.restype = I
     lib.spec_append_kv_packed.argtypes = [P, P, P, L, L, L, P, P, F, P, I, I, I, P, I, P, P, P, I, I, I, KV, P, I, P, P, P]
     lib.spec_append_kv_packed.restype = I
-    lib.sv_attend_packed_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    lib.sv_attend_packed_workspace_bytes.argtypes = [I, I, I, I, I, I, I, I]
     lib.sv_attend_packed_workspace_bytes.restype = Z
     lib.spec_attend_packed.argtypes = [P, L, KV, P, I, P, P, I, I, I, F, P, P, P, P, Z, P]
     lib.spec_attend_packed.restype = I
@@ -1064,8 +1064,8 @@ def spec_append_kv_packed(q, k, v, cache, page_table, starts, base=None, positio
 
 
 @functools.lru_cache(maxsize=4096)
-def attend_packed_workspace_bytes(T, B, H, kv_heads, head_dim, P, page_size) -> int:
-    return int(load_library().sv_attend_packed_workspace_bytes(T, B, H, kv_heads, head_dim, P, page_size))
+def attend_packed_workspace_bytes(T, B, H, kv_heads, head_dim, P, page_size, dtype_code) -> int:
+    return int(load_library().sv_attend_packed_workspace_bytes(T, B, H, kv_heads, head_dim, P, page_size, dtype_code))
 
 
 def spec_attend_packed(q, cache, page_table, starts, base=None, *, scale=None, out=None, lse=False, status=True,
@@ -1090,7 +1090,8 @@ def spec_attend_packed(q, cache, page_table, starts, base=None, *, scale=None, o
         res["lse"] = _window_out(torch, None if lse is True else lse, "lse", (T, H), torch.float32, dev)
     if status:
         res["status"] = torch.empty(B, dtype=torch.int32, device=dev)
-    ws = _workspace(torch, attend_packed_workspace_bytes(T, B, H, cache.kv_heads, D, P, cache.page_size), dev, workspace)
+    ws = _workspace(torch, attend_packed_workspace_bytes(T, B, H, cache.kv_heads, D, P, cache.page_size, cache._c.dt), dev,
+                    workspace)
     rc = _call(
         torch, lib.spec_attend_packed, dev, stream, q.data_ptr(), qs, cache._c, page_table.data_ptr(), P,
         starts.data_ptr(), _ptr(base), T, B, H, float(D ** -0.5 if scale is None else scale), res["out"].data_ptr(),

@@ -931,11 +931,11 @@ bool stride_ok(long long stride, long long least, bool several) {
     return stride % 8 == 0 && (stride >= least || !several);
 }
 
-bool packed_sizes_ok(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size) {
+bool packed_sizes_ok(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size, bool e4m3) {
     if (!paged_sizes_ok(page_size, head_dim) || static_cast<long long>(P) * page_size > kMaxSlots) return false;
     if (H > 65536 || static_cast<double>(T) * H > 2.0e9) return false;
     if (B == 0) return true;
-    const PackedPlan p = packed_plan(T, B, H, kv_heads, head_dim, P, page_size);
+    const PackedPlan p = packed_plan(T, B, H, kv_heads, head_dim, P, page_size, e4m3);
     return packed_groups(kv_heads, p) <= kMaxGroups && packed_join_groups(kv_heads, head_dim, p) <= kMaxGroups;
 }
 
@@ -1079,11 +1079,13 @@ sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, lon
     return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
-size_t sv_attend_packed_workspace_bytes(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size) {
-    if (T < 0 || B < 1 || H < 1 || kv_heads < 1 || P < 1 || H % kv_heads != 0 ||
-        !packed_sizes_ok(T, B, H, kv_heads, head_dim, P, page_size))
+size_t sv_attend_packed_workspace_bytes(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size,
+                                        sv_dtype cache_dt) {
+    const bool e4m3 = cache_dt == SV_E4M3;
+    if ((cache_dt != SV_BF16 && !e4m3) || T < 0 || B < 1 || H < 1 || kv_heads < 1 || P < 1 || H % kv_heads != 0 ||
+        !packed_sizes_ok(T, B, H, kv_heads, head_dim, P, page_size, e4m3))
         return 0;
-    return std::max<size_t>(256, packed_plan(T, B, H, kv_heads, head_dim, P, page_size).total);
+    return std::max<size_t>(256, packed_plan(T, B, H, kv_heads, head_dim, P, page_size, e4m3).total);
 }
 
 sv_status spec_attend_packed(const void *q, long long q_stride, sv_paged_kv cache, const int32_t *page_table, int P,
@@ -1095,7 +1097,8 @@ sv_status spec_attend_packed(const void *q, long long q_stride, sv_paged_kv cach
     if (T < 0 || B < 0 || H < 1 || H % cache.kv_heads != 0 || !(scale > 0.0f) || !isfinite(scale))
         return SV_ERR_INVALID_ARG;
     const int D = cache.head_dim;
-    if (!packed_sizes_ok(T, B, H, cache.kv_heads, D, P, cache.page_size)) return SV_ERR_UNSUPPORTED;
+    const bool e4m3 = cache.dt == SV_E4M3;
+    if (!packed_sizes_ok(T, B, H, cache.kv_heads, D, P, cache.page_size, e4m3)) return SV_ERR_UNSUPPORTED;
     if (B == 0) return SV_OK;
     if (!page_table || !starts || (T > 0 && (!q || !out)) || !workspace) return SV_ERR_INVALID_ARG;
     st = check_cache_pointers(cache);
@@ -1103,7 +1106,7 @@ sv_status spec_attend_packed(const void *q, long long q_stride, sv_paged_kv cach
     if (!aligned16(q) || !aligned16(out) || !aligned256(workspace)) return SV_ERR_INVALID_ARG;
     if (!stride_ok(q_stride, static_cast<long long>(H) * D, T > 1)) return SV_ERR_INVALID_ARG;
     if (q_stride > 1LL << 31) return SV_ERR_UNSUPPORTED;
-    const PackedPlan p = packed_plan(T, B, H, cache.kv_heads, D, P, cache.page_size);
+    const PackedPlan p = packed_plan(T, B, H, cache.kv_heads, D, P, cache.page_size, e4m3);
     if (workspace_bytes < std::max<size_t>(256, p.total)) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
     PackedArgs a = {};
@@ -1134,7 +1137,7 @@ sv_status spec_attend_packed(const void *q, long long q_stride, sv_paged_kv cach
     a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
     a.part_bad = reinterpret_cast<int32_t *>(ws + p.part_bad);
     if (!isfinite(a.c)) return SV_ERR_UNSUPPORTED;
-    const bool e4m3 = cache.dt == SV_E4M3;
+    a.unit = e4m3 ? 1.0f : a.c;  // an e4m3 cache's scores are scaled one by one anyway
     hipError_t e = traced(SV_K_ATTEND_PACKED, stream, [&] { return launch_attend_packed(a, D, e4m3, p, stream); });
     if (e == hipSuccess && p.S > 1)
         e = traced(SV_K_ATTEND_PACKED_JOIN, stream, [&] { return launch_attend_packed_join(a, D, p, stream); });

@@ -40,7 +40,6 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kSlots = 64;         // slots of a tile
-constexpr int kGroupRows = 128;    // rows of a workgroup
 constexpr float kSlack = 8.0f;     // weights may reach 2^kSlack before the reference moves
 // The reference of a row that has met no score.
 constexpr float kNoRef = -3.4028234663852886e38f;
@@ -125,8 +124,8 @@ __device__ __forceinline__ void pin(float &x) { asm volatile("" : "+v"(x)); }
 
 // The row tile a workgroup takes: rows [r0, r0 + rows of a workgroup) of request b.
 struct Unit {
-    int b, tile, first, count;  // request, its tile, its first token and its tokens
-    bool last;                  // the request's last tile
+    int b, tile, first, count, base;  // request, its tile, first token, tokens, and cached ones before
+    bool last;                        // the request's last tile
 };
 // Row tiles of a request of `count` tokens.
 __device__ __forceinline__ int tiles_of(int count, int G, int rows) {
@@ -143,8 +142,11 @@ __device__ __forceinline__ int request_tokens(const PackedArgs &a, int i, int *f
 __device__ __forceinline__ Unit find_unit(const PackedArgs &a, int u, int rows, int lane) {
     long long before = 0;
     for (int i0 = 0; i0 < a.B; i0 += kWave) {
-        int first = 0, count = 0;
-        if (i0 + lane < a.B) count = request_tokens(a, i0 + lane, &first);
+        int first = 0, count = 0, base = 0;
+        if (i0 + lane < a.B) {
+            count = request_tokens(a, i0 + lane, &first);
+            if (a.base) base = a.base[i0 + lane];
+        }
         const int mine = tiles_of(count, a.G, rows);
         long long up = mine;
 #pragma unroll
@@ -159,6 +161,7 @@ __device__ __forceinline__ Unit find_unit(const PackedArgs &a, int u, int rows, 
             r.b = i0 + at;
             r.count = uniform(__shfl(count, at, kWave));
             r.first = uniform(__shfl(first, at, kWave));
+            r.base = uniform(__shfl(base, at, kWave));
             const int tiles = uniform(__shfl(mine, at, kWave));
             r.tile = uniform(static_cast<int>(u - before - (__shfl(up, at, kWave) - tiles)));
             r.last = r.tile == tiles - 1;
@@ -166,7 +169,7 @@ __device__ __forceinline__ Unit find_unit(const PackedArgs &a, int u, int rows, 
         }
         before += __shfl(up, kWave - 1, kWave);
     }
-    return Unit{-1, 0, 0, 0, false};
+    return Unit{-1, 0, 0, 0, 0, false};
 }
 
 // Splits of a row tile whose rows see `tiles` tiles of slots: as many as have a
@@ -185,9 +188,10 @@ __device__ __forceinline__ int v_chunk(int r, int c) {
     return D == 64 ? c ^ (2 * (r & 3)) : c ^ (4 * (r & 3)) ^ (2 * ((r >> 1) & 1));
 }
 
-template <int D, bool E4M3>
-__global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(PackedArgs a) {
-    constexpr int kRows = kGroupRows;             // of a workgroup
+template <int D, bool E4M3, int WAVES>
+__global__ __launch_bounds__(WAVES *kWave, D > 128 ? 1 : 2) void k_attend_packed(PackedArgs a) {
+    constexpr int kThreads = WAVES * kWave;
+    constexpr int kRows = 32 * WAVES;             // of a workgroup
     constexpr int kSteps = D / 16;                // of the first product
     constexpr int kVals = D / 32;                 // 32-value blocks of a row of V
     constexpr int kRowB = D * 2;                  // bytes of a row in LDS
@@ -200,7 +204,7 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
     const int half = lane >> 5, col = lane & 31;
 
     if (blockIdx.x == 0 && a.status) {  // requests without rows, or with malformed bounds
-        for (int b = threadIdx.x; b < a.B; b += kBlock) {
+        for (int b = threadIdx.x; b < a.B; b += kThreads) {
             int first;
             if (request_tokens(a, b, &first) == 0) a.status[b] = first == a.starts[b + 1] && first >= 0 && first <= a.T ? 0 : 2;
         }
@@ -210,7 +214,7 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
     const int split = rest % a.S, u = a.units - 1 - rest / a.S;
     const Unit un = find_unit(a, u, kRows, lane);
     if (un.b < 0) return;
-    const int base = a.base ? uniform(a.base[un.b]) : 0;
+    const int base = un.base;
     const long long r0 = static_cast<long long>(un.tile) * kRows;
     const int rows = static_cast<int>(min(static_cast<long long>(un.count) * a.G - r0, static_cast<long long>(kRows)));
     // slots that exist, and the slots that the tile's first and last row see
@@ -263,12 +267,13 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
 
     // ---- rows from memory to LDS: V's stage holds a tile; K's window j, half a tile
-    // earlier, the 64 slots from 64 j - 32 on.  Wave w brings the w-th 16 of them, which
-    // lie in one page; a bf16 cache's straight into LDS, an e4m3 cache's through registers
+    // earlier, the 64 slots from 64 j - 32 on.  Wave w brings the w-th 16 (of eight waves:
+    // 8) of them, which lie in one page; a bf16 cache's straight into LDS, an e4m3 cache's through registers
     const int32_t *table = a.page_table + static_cast<long long>(un.b) * a.P;
     const int page_mask = (1 << a.page_shift) - 1;
     constexpr int kLaneRows = kWave / kRowChunks;  // rows that one load of a wave covers
-    constexpr int kLoads = 16 / kLaneRows;
+    constexpr int kWaveRows = kSlots / WAVES, kLoads = kWaveRows / kLaneRows;
+    static_assert(kLoads >= 1, "a wave's rows fill its loads");
     constexpr int kTileB = kSlots * kRowB;
     const int row_in = lane / kRowChunks, chunk = lane % kRowChunks;
     struct Stream {
@@ -288,20 +293,20 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
                 s.ids = 0;
             }
         }
-        const int page = __builtin_amdgcn_readlane(s.ids, group0 + w - (s.end - kWave));
-        const long long row = ((static_cast<long long>(page) * a.Hkv + h) << a.page_shift) + ((slot + 16 * w) & page_mask);
+        const int page = __builtin_amdgcn_readlane(s.ids, group0 + kWaveRows * w / 16 - (s.end - kWave));
+        const long long row = ((static_cast<long long>(page) * a.Hkv + h) << a.page_shift) + ((slot + kWaveRows * w) & page_mask);
         const char *from = static_cast<const char *>(pages) + row * (D * kElem);
         if constexpr (E4M3) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) s.x[i] = *reinterpret_cast<const u32x4 *>(from + (i * kLaneRows + row_in) * (D * kElem) + chunk * 16);
-            s.scale = scale[row + (lane & 15)];
+            s.scale = scale[row + lane % kWaveRows];
         } else {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int r = i * kLaneRows + row_in;  // place `chunk` of the row holds chunk
-                const int c = is_k ? k_chunk<D>(r, chunk) : v_chunk<D>(r, chunk);
+                const int r = i * kLaneRows + row_in, at = kWaveRows * w + r;
+                const int c = is_k ? k_chunk<D>(at, chunk) : v_chunk<D>(at, chunk);  // what place `chunk` holds
                 __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)(from + r * kRowB + c * 16),
-                                                 (SV_LDS void *)(stage + w * 16 * kRowB + i * 1024), 16, 0, 0);
+                                                 (SV_LDS void *)(stage + kWaveRows * w * kRowB + i * 1024), 16, 0, 0);
             }
         }
     };
@@ -312,7 +317,7 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
     auto store = [&](Stream &s, char *stage, float *scale, bool is_k) {  // e4m3: widened
 #pragma unroll
         for (int i = 0; i < (E4M3 ? kLoads : 0); ++i) {
-            const int r = 16 * w + i * kLaneRows + row_in;
+            const int r = kWaveRows * w + i * kLaneRows + row_in;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 u32x4 y;
@@ -325,20 +330,33 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
                 *reinterpret_cast<u32x4 *>(stage + r * kRowB + c * 16) = y;
             }
         }
-        if (lane < 16) scale[16 * w + lane] = s.scale;
+        if (lane < kWaveRows) scale[kWaveRows * w + lane] = s.scale;
+    };
+    auto note_odd = [&](int tile) {
+        atomicMin(&odd_tile[0], tile);
+        atomicMax(&odd_tile[1], tile);
     };
     auto store_k = [&](int window) {
-        if constexpr (E4M3) store(ks, kv[0][(window - t0) & 1], scales[0][(window - t0) & 1], true);
+        if constexpr (E4M3) {
+            ks.scale *= a.c;
+            store(ks, kv[0][(window - t0) & 1], scales[0][(window - t0) & 1], true);
+        }
     };
     auto store_v = [&](int tile) {
-        if constexpr (E4M3) store(vs, kv[1][(tile - t0) & 1], scales[1][(tile - t0) & 1], false);
+        if constexpr (E4M3) {
+            if ((tile + 1) * kSlots > least && !isfinite(vs.scale)) {  // as a value is, in clean_v
+                vs.scale = 0.0f;
+                note_odd(tile);
+            }
+            store(vs, kv[1][(tile - t0) & 1], scales[1][(tile - t0) & 1], false);
+        }
     };
     // A tile's values that some row does not see: those behind the last slot zeroed, and
     // what is not finite left out (and noted)
     auto clean_v = [&](int tile) {
         char *stage = kv[1][(tile - t0) & 1];
         bool odd = false;
-        for (int i = threadIdx.x; i < kTileB / 16; i += kBlock) {
+        for (int i = threadIdx.x; i < kTileB / 16; i += kThreads) {
             u32x4 y = *reinterpret_cast<u32x4 *>(stage + i * 16);
             const bool behind = tile * kSlots + i / (kRowB / 16) >= total;
 #pragma unroll
@@ -349,10 +367,7 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
             }
             *reinterpret_cast<u32x4 *>(stage + i * 16) = y;
         }
-        if (odd) {
-            atomicMin(&odd_tile[0], tile);
-            atomicMax(&odd_tile[1], tile);
-        }
+        if (odd) note_odd(tile);
     };
 
     // ---- the parts of a half tile's work; slot 64 tile + 32 f + 8 (e / 4) + 4 half + e % 4
@@ -389,28 +404,36 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
     f32x16 minus;
 #pragma unroll
     for (int e = 0; e < 16; ++e) minus[e] = 0.0f;
+    // Fragments on their way: a phase asks for the first of the next while it ends, so none
+    // begins with a wait.  Entry n of a phase goes to place n % (kAhead + 1).
+    u32x4 kf[kAhead + 1];
+    Turned vf[kAhead + 1];
+    auto ask_k = [&](auto par, auto f, auto n) {  // of the products that half f's weights run beside
+        kf[decltype(n)::value % (kAhead + 1)] = k_part(Index<1 - decltype(par)::value>{}, f, n);
+    };
+    auto ask_v = [&](auto par, auto f, auto n) { vf[decltype(n)::value % (kAhead + 1)] = v_part(par, f, n); };
     // A half's weights out of its scores (relative to the reference), and the next half's
     // products, a product to a few weights.  The sums of a bf16 cache begin at minus the
     // reference: what leaves them is already relative to it.
-    auto weigh = [&](auto par, auto f, int tile, f32x16 &s, f32x16 &next, bf16x8 (&p)[2]) {
-        constexpr int F = decltype(f)::value, kWindow = 1 - decltype(par)::value;
-        const int seen = sees - tile * kSlots - 4 * half;
-        u32x4 kf[kAhead + 1];
-        unrolled<0, kAhead>([&](auto c) { kf[decltype(c)::value] = k_part(Index<kWindow>{}, f, c); });
+    auto weigh = [&](auto par, auto f, f32x16 &s, f32x16 &next, bf16x8 (&p)[2]) {
+        constexpr int F = decltype(f)::value;
         float sum[2] = {0, 0};
         f32x4 vs4;
         unrolled<0, kSteps>([&](auto cc) {
             constexpr int c = decltype(cc)::value, kPer = 16 / kSteps;
-            if constexpr (c + kAhead < kSteps) kf[(c + kAhead) % (kAhead + 1)] = k_part(Index<kWindow>{}, f, Index<c + kAhead>{});
-            arrived<(kSteps - 1 - c < kAhead ? kSteps - 1 - c : kAhead)>(kf[c % (kAhead + 1)]);
+            constexpr int kLeft = kSteps - 1 - c < kAhead ? kSteps - 1 - c : kAhead;  // K's fragments behind this one
+            if constexpr (c + kAhead < kSteps)
+                ask_k(par, f, Index<c + kAhead>{});
+            else
+                ask_v(par, f, Index<c + kAhead - kSteps>{});
+            arrived<kLeft + 2 * (kAhead - kLeft)>(kf[c % (kAhead + 1)]);
             next = mfma32(__builtin_bit_cast(bf16x8, kf[c % (kAhead + 1)]), q[c], c == 0 ? minus : next);
             unrolled<0, kPer>([&](auto xx) {
                 constexpr int e = c * kPer + decltype(xx)::value;
                 if constexpr (E4M3 && e % 4 == 0) vs4 = vscale[decltype(par)::value * (kSlots / 4) + 8 * F + 2 * (e / 4)];
-                float y = fast_exp2(s[e] * a.c);
+                float y = fast_exp2(E4M3 ? s[e] : s[e] * a.unit);
                 sum[e % 2] += y;
-                // a masked slot's scale may be anything
-                if constexpr (E4M3) y = 32 * F + 8 * (e / 4) + e % 4 >= seen ? 0.0f : y * vs4[e % 4];
+                if constexpr (E4M3) y *= vs4[e % 4];
                 s[e] = y;
                 if constexpr (e % 8 == 7)
                     p[e / 8] = as_bf16x8(pack_bf16(s[e - 7], s[e - 6]), pack_bf16(s[e - 5], s[e - 4]), pack_bf16(s[e - 3], s[e - 2]),
@@ -423,18 +446,20 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
         l += sum[0] + sum[1];
     };
     // The half's values mixed, and the next half's largest score (an e4m3 cache's scores
-    // scaled and made relative first)
+    // scaled, into units of log2, and made relative first)
     auto mix = [&](auto par, auto f, const bf16x8 (&p)[2], f32x16 &next) {
         constexpr int F = decltype(f)::value, kWindow = 1 - decltype(par)::value;
-        Turned vf[kAhead + 1];
-        unrolled<0, kAhead>([&](auto i) { vf[decltype(i)::value] = v_part(par, f, i); });
         float most = -__builtin_huge_valf();
         f32x4 ks4;
         unrolled<0, kMixes>([&](auto ii) {
             constexpr int i = decltype(ii)::value, g = i / kVals, d = i % kVals;
-            if constexpr (i + kAhead < kMixes) vf[(i + kAhead) % (kAhead + 1)] = v_part(par, f, Index<i + kAhead>{});
+            constexpr int kLeft = kMixes - 1 - i < kAhead ? kMixes - 1 - i : kAhead;
+            if constexpr (i + kAhead < kMixes)
+                ask_v(par, f, Index<i + kAhead>{});
+            else if constexpr (F == 0)  // the second half's window is there already
+                ask_k(par, Index<1>{}, Index<i + kAhead - kMixes>{});
             Turned &v = vf[i % (kAhead + 1)];
-            arrived<2 * (kMixes - 1 - i < kAhead ? kMixes - 1 - i : kAhead)>(v.lo, v.hi);
+            arrived<2 * kLeft + (F == 0 ? kAhead - kLeft : 0)>(v.lo, v.hi);
             o[d] = mfma32(as_bf16x8(v.lo.x, v.lo.y, v.hi.x, v.hi.y), p[g], o[d]);
             if constexpr (i >= kVals) {  // the scores are there by now
                 constexpr int kPairs = 8 / kVals;
@@ -466,14 +491,14 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
     };
     // Moves the references where a score is far above its own, and to a row's first score
     auto refer = [&](float most, f32x16 &s) {
-        const bool moves = m == kNoRef ? most > -__builtin_huge_valf() : most * a.c > kSlack;
+        const bool moves = m == kNoRef ? most > -__builtin_huge_valf() : most * a.unit > kSlack;
         if (__ballot(moves) == 0) return;
         const float up = pair_max(most);
         const bool first = m == kNoRef;
         const float by = first ? (up > -__builtin_huge_valf() ? up : 0.0f) : fmaxf(up, 0.0f);
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] -= by;
-        const float f = first ? 1.0f : fast_exp2(-by * a.c);  // a first reference has nothing to turn
+        const float f = first ? 1.0f : fast_exp2(-by * a.unit);  // a first reference has nothing to turn
         l *= f;
 #pragma unroll
         for (int i = 0; i < kVals; ++i) o[i] *= f;
@@ -532,12 +557,13 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
         }
         if (tile < wave_end) {
             bf16x8 p[2];
+            unrolled<0, kAhead>([&](auto n) { ask_k(par, Index<0>{}, n); });
             refer(most, s);
-            weigh(par, Index<0>{}, tile, s, next, p);
+            weigh(par, Index<0>{}, s, next, p);
             most = mix(par, Index<0>{}, p, next);
             if ((tile + 1) * kSlots > wave_least) most = masked(tile * kSlots + 32, next);
             refer(most, next);
-            weigh(par, Index<1>{}, tile, next, s, p);
+            weigh(par, Index<1>{}, next, s, p);
             most = mix(par, Index<1>{}, p, s);
             if ((tile + 2) * kSlots > wave_least) most = masked((tile + 1) * kSlots, s);
         }
@@ -572,15 +598,14 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
 #pragma unroll
                 for (int e = 0; e < 8; ++e) score += static_cast<float>(q[c][e]) * value(a.k_pages, 16 * c + 8 * half + e);
             score = pair_sum(score);
-            if constexpr (E4M3) score *= a.k_scale[row];
+            if constexpr (E4M3) score *= a.k_scale[row] * a.c;
             if (slot >= sees) continue;
-            float weight = fast_exp2((score - m) * a.c);
-            if constexpr (E4M3) weight *= a.v_scale[row];
+            const float weight = fast_exp2((score - m) * a.unit), scale = E4M3 ? a.v_scale[row] : 1.0f;
 #pragma unroll
             for (int d = 0; d < kVals; ++d)
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    const float v = value(a.v_pages, d * 32 + 8 * (x / 4) + 4 * half + x % 4);
+                    const float v = value(a.v_pages, d * 32 + 8 * (x / 4) + 4 * half + x % 4) * scale;
                     if (!isfinite(v)) o[d][x] += weight * v;
                 }
         }
@@ -604,7 +629,7 @@ __global__ __launch_bounds__(kBlock, D > 128 ? 1 : 2) void k_attend_packed(Packe
         const bool none = first_bad < sees;
         const float f = none ? 0.0f : 1.0f / L;
         const long long to = static_cast<long long>(token) * a.H + head;
-        if (a.lse && half == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m, L, a.c);
+        if (a.lse && half == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m, L, a.unit);
         uint16_t *dst = a.out + to * D + 4 * half;
 #pragma unroll
         for (int d = 0; d < kVals; ++d)
@@ -640,7 +665,7 @@ __global__ __launch_bounds__(kBlock) void k_packed_join(PackedArgs a, int rows_p
     const int h = rest % a.Hkv, u = rest / a.Hkv;
     const Unit un = find_unit(a, u, rows_per, lane);
     if (un.b < 0) return;
-    const int base = a.base ? uniform(a.base[un.b]) : 0;
+    const int base = un.base;
     const long long r0 = static_cast<long long>(un.tile) * rows_per;
     const int rows = static_cast<int>(min(static_cast<long long>(un.count) * a.G - r0, static_cast<long long>(rows_per)));
     const long long exist = static_cast<long long>(a.P) << a.page_shift;
@@ -662,13 +687,13 @@ __global__ __launch_bounds__(kBlock) void k_packed_join(PackedArgs a, int rows_p
     for (int s = 0; s < active; ++s) {
         const long long row = (unit + s) * rows_per + r;
         const float ms = a.part_ml[row * 2], ls = a.part_ml[row * 2 + 1];
-        const float f = ms == kNoRef ? 0.0f : fast_exp2((ms - m) * a.c);
+        const float f = ms == kNoRef ? 0.0f : fast_exp2((ms - m) * a.unit);
         L += ls * f;
         o += *reinterpret_cast<const f32x4 *>(a.part_o + row * D + d) * f;
     }
     const bool none = first_bad < static_cast<long long>(base) + j + 1;
     const long long to = static_cast<long long>(un.first + j) * a.H + h * a.G + g;
-    if (a.lse && d == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m, L, a.c);
+    if (a.lse && d == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m, L, a.unit);
     const float f = none ? 0.0f : 1.0f / L;
     if (none) o = f32x4{0, 0, 0, 0};
     *reinterpret_cast<u32x2 *>(a.out + to * D + d) = u32x2{pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f)};
@@ -676,11 +701,16 @@ __global__ __launch_bounds__(kBlock) void k_packed_join(PackedArgs a, int rows_p
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+template <int D, bool E4M3>
+hipError_t launch_waves(const PackedArgs &a, const PackedPlan &p, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(packed_groups(a.Hkv, p)));
+    if constexpr (D == 128 && E4M3)
+        if (p.rows == 256) return launch_kernel(k_attend_packed<D, E4M3, 8>, grid, dim3(8 * kWave), 0, s, a);
+    return launch_kernel(k_attend_packed<D, E4M3, 4>, grid, dim3(4 * kWave), 0, s, a);
+}
 template <int D>
 hipError_t launch_d(const PackedArgs &a, bool e4m3, const PackedPlan &p, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(packed_groups(a.Hkv, p)));
-    return e4m3 ? launch_kernel(k_attend_packed<D, true>, grid, dim3(kBlock), 0, s, a)
-                : launch_kernel(k_attend_packed<D, false>, grid, dim3(kBlock), 0, s, a);
+    return e4m3 ? launch_waves<D, true>(a, p, s) : launch_waves<D, false>(a, p, s);
 }
 
 }  // namespace
@@ -691,15 +721,23 @@ long long packed_join_groups(int Hkv, int D, const PackedPlan &p) {
     return p.S == 1 ? 0 : static_cast<long long>(p.units) * Hkv * (p.rows / (kBlock / (D / 4)));
 }
 
-PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size) {
+// An e4m3 cache's rows are widened once by each workgroup, so with heads of 128 eight
+// waves share them where the rows fill the card (512 tokens over 16000: 190 us, and 203
+// with four; heads of 64 leave eight waves less than a load each, 256 one wave a SIMD).
+constexpr long long kCus = 256;
+bool eight_waves(long long rows, int Hkv, int D, bool e4m3) { return e4m3 && D == 128 && rows * Hkv >= kCus * 64; }
+
+PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size, bool e4m3) {
     PackedPlan p = {};
     const long long all = static_cast<long long>(T) * (H / Hkv);
-    p.rows = kGroupRows;
+    const bool eight = eight_waves(all, Hkv, D, e4m3);
+    p.rows = eight ? 256 : 128;
     // every request may end in a part of a tile; none has more tiles than rows
     p.units = static_cast<int>(std::max(1LL, std::min(all / p.rows + B, all)));
     const long long tiles = (static_cast<long long>(P) * page_size + kSlots - 1) / kSlots;
     const long long groups = static_cast<long long>(p.units) * Hkv;
-    long long S = std::max(1LL, 512 / std::max(1LL, groups));
+    // two workgroups of four waves, or one of eight, for each compute unit
+    long long S = std::max(1LL, kCus * (eight ? 1 : 2) / std::max(1LL, groups));
     S = std::min(S, std::max(1LL, tiles / kLeastRun));
     const size_t per = static_cast<size_t>(groups) * p.rows * (D + 2) * 4;
     while (S > 1 && per * S > (size_t{512} << 20)) --S;

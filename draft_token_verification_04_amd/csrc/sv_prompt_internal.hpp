@@ -52,6 +52,7 @@ struct PackedArgs {
     const int32_t *page_table, *starts, *base;  // base may be null: no cached tokens
     int T, B, H, Hkv, G, P, page_shift, num_pages;
     float c;            // scale * log2(e)
+    float unit;         // log2(e) in the units of the scores that a row's reference is held in
     uint16_t *out;      // [T][H][D]
     float *lse;         // [T][H] or null
     int32_t *status;    // [B] or null
@@ -64,7 +65,7 @@ struct PackedPlan {
     int units, S;
     size_t part_o, part_ml, part_bad, total;
 };
-PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size);
+PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size, bool e4m3);
 long long packed_groups(int Hkv, const PackedPlan &p);  // workgroups of the launches
 long long packed_join_groups(int Hkv, int D, const PackedPlan &p);
 hipError_t launch_attend_packed(const PackedArgs &a, int D, bool e4m3, const PackedPlan &p, hipStream_t s);

@@ -600,7 +600,8 @@ sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, lon
  * Workspace: sv_attend_packed_workspace_bytes (0 for invalid or unsupported sizes), at
  * most about 512 MB.
  */
-size_t sv_attend_packed_workspace_bytes(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size);
+size_t sv_attend_packed_workspace_bytes(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size,
+                                        sv_dtype cache_dt);
 
 sv_status spec_attend_packed(const void *q, long long q_stride, sv_paged_kv cache, const int32_t *page_table, int P,
                              const int32_t *starts, const int32_t *base, int T, int B, int H, float scale, void *out,

@@ -114,14 +114,14 @@ def test_attend_packed_refusals(lib):
     assert _attend(lib, scale=3e38, wsb=1 << 30) == UNS
     assert _attend(lib, B=0, q=None, ws=None) == sv.SV_OK
     f = lib.sv_attend_packed_workspace_bytes
-    need = f(7, 2, 4, 2, 128, 5, 16)
+    need = f(7, 2, 4, 2, 128, 5, 16, sv.SV_BF16)
     assert need >= 256 and need % 256 == 0 and _attend(lib, wsb=need - 1) == WS
-    assert f(7, 0, 4, 2, 128, 5, 16) == 0 and f(7, 2, 5, 2, 128, 5, 16) == 0 and f(7, 2, 4, 2, 96, 5, 16) == 0
-    assert f(-1, 2, 4, 2, 128, 5, 16) == 0 and f(7, 2, 4, 2, 128, 1 << 28, 16) == 0
+    assert f(7, 0, 4, 2, 128, 5, 16, sv.SV_BF16) == 0 and f(7, 2, 5, 2, 128, 5, 16, sv.SV_BF16) == 0 and f(7, 2, 4, 2, 96, 5, 16, sv.SV_BF16) == 0
+    assert f(-1, 2, 4, 2, 128, 5, 16, sv.SV_BF16) == 0 and f(7, 2, 4, 2, 128, 1 << 28, 16, sv.SV_BF16) == 0
     # few rows over a long table are split, within the bound; many rows are not
-    assert 256 < f(200, 1, 32, 8, 128, 8192, 16) <= 513 << 20
-    assert f(20000, 4, 32, 8, 128, 8192, 16) == 256
-    assert f(64, 64, 64, 64, 256, 1 << 20, 16) <= 513 << 20
+    assert 256 < f(200, 1, 32, 8, 128, 8192, 16, sv.SV_BF16) <= 513 << 20
+    assert f(20000, 4, 32, 8, 128, 8192, 16, sv.SV_BF16) == 256
+    assert f(64, 64, 64, 64, 256, 1 << 20, 16, sv.SV_BF16) <= 513 << 20
 
 
 def test_constants_match_the_header():

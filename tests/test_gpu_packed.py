@@ -65,7 +65,7 @@ def test_chunks_over_long_contexts_are_split_and_joined(kind):
         table[b, :used], ids = ids[:used], ids[used:]
     table[1, 90] = 2 * P  # the second request's last slots lie on a page that does not exist
     cache = Cache(rng, 2 * P, Hkv, page, 128, kind)
-    assert sv.attend_packed_workspace_bytes(T, 4, H, Hkv, 128, P, page) > 256
+    assert sv.attend_packed_workspace_bytes(T, 4, H, Hkv, 128, P, page, sv.SV_BF16 if kind == "bf16" else sv.SV_E4M3) > 256
     g, o = run_packed(rng, cache, table, starts, base, T, H)
     assert o["status"].tolist() == [0, 1, 0, 0]
     check_attend(g, o, 9040)
