@@ -624,13 +624,16 @@ __global__ __launch_bounds__(WAVES *kWave, D > 128 ? 1 : 2) void k_attend_packed
         }
     }
     const float L = pair_sum(l);
-    if (!live) return;
     if (alone) {
         const bool none = first_bad < sees;
         const float f = none ? 0.0f : 1.0f / L;
         const long long to = static_cast<long long>(token) * a.H + head;
-        if (a.lse && half == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m, L, a.unit);
-        uint16_t *dst = a.out + to * D + 4 * half;
+        if (live && a.lse && half == 0) a.lse[to] = none ? -__builtin_huge_valf() : log_sum(m, L, a.unit);
+        // turned in LDS (the wave's own 32 rows of the first stages, chunk c of row r at
+        // c ^ r), so that rows leave whole (16 prompts, 143 MB of them: 335 us, and 343 as
+        // pieces of 16 bytes of 32 rows)
+        constexpr int kChunks = kRowB / 16, kPer = kWave / kChunks;  // of a row; rows a store covers
+        char *room = &kv[0][0][0] + w * 32 * kRowB;
 #pragma unroll
         for (int d = 0; d < kVals; ++d)
 #pragma unroll
@@ -638,9 +641,20 @@ __global__ __launch_bounds__(WAVES *kWave, D > 128 ? 1 : 2) void k_attend_packed
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : o[d][4 * x + e] * f;
-                *reinterpret_cast<u32x2 *>(dst + d * 32 + 8 * x) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                *reinterpret_cast<u32x2 *>(room + col * kRowB + ((4 * d + x) ^ (col & (kChunks - 1))) * 16 + 8 * half) =
+                    u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
             }
-    } else {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const int place = lane % kChunks;
+#pragma unroll
+        for (int i = 0; i < 32 / kPer; ++i) {
+            const int row = i * kPer + lane / kChunks;  // whose lanes know where it goes
+            const long long dst = __shfl(to, row, kWave);
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(room + row * kRowB + place * 16);
+            if (w * 32 + row < rows)
+                *reinterpret_cast<u32x4 *>(a.out + dst * D + (place ^ (row & (kChunks - 1))) * 8) = v;
+        }
+    } else if (live) {
         const long long row = unit * kRows + r;
         if (half == 0) {
             a.part_ml[row * 2] = m;
