@@ -137,6 +137,16 @@ __device__ __forceinline__ int request_tokens(const PackedArgs &a, int i, int *f
     *first = lo;
     return lo >= 0 && hi >= lo && hi <= a.T ? hi - lo : 0;
 }
+// The sum over the wave's lanes up to this one.
+__device__ __forceinline__ long long running_sum(int mine, int lane) {
+    long long up = mine;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const long long y = __shfl_up(up, o, kWave);
+        if (lane >= o) up += y;
+    }
+    return up;
+}
 // The u-th row tile, requests in order, or b = -1 behind the last.  A wave sums the
 // tiles of 64 requests at a time.
 __device__ __forceinline__ Unit find_unit(const PackedArgs &a, int u, int rows, int lane) {
@@ -148,12 +158,7 @@ __device__ __forceinline__ Unit find_unit(const PackedArgs &a, int u, int rows, 
             if (a.base) base = a.base[i0 + lane];
         }
         const int mine = tiles_of(count, a.G, rows);
-        long long up = mine;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const long long y = __shfl_up(up, o, kWave);
-            if (lane >= o) up += y;
-        }
+        const long long up = running_sum(mine, lane);
         const uint64_t past = __ballot(before + up > u);
         if (past) {
             const int at = __ffsll(static_cast<long long>(past)) - 1;
@@ -203,10 +208,22 @@ __global__ __launch_bounds__(WAVES *kWave, D > 128 ? 1 : 2) void k_attend_packed
     const int lane = threadIdx.x & (kWave - 1), w = uniform(static_cast<int>(threadIdx.x >> 6));
     const int half = lane >> 5, col = lane & 31;
 
-    if (blockIdx.x == 0 && a.status) {  // requests without rows, or with malformed bounds
-        for (int b = threadIdx.x; b < a.B; b += kThreads) {
-            int first;
-            if (request_tokens(a, b, &first) == 0) a.status[b] = first == a.starts[b + 1] && first >= 0 && first <= a.T ? 0 : 2;
+    // requests without rows, with malformed bounds, or (where bounds overlap) behind the
+    // last row tile of the launch
+    if (blockIdx.x == 0 && a.status && w == 0) {
+        long long before = 0;
+        for (int i0 = 0; i0 < a.B; i0 += kWave) {
+            const int b = i0 + lane;
+            int first = 0;
+            const int count = b < a.B ? request_tokens(a, b, &first) : 0;
+            const long long up = before + running_sum(tiles_of(count, a.G, kRows), lane);
+            if (b < a.B) {
+                if (count == 0)
+                    a.status[b] = first == a.starts[b + 1] && first >= 0 && first <= a.T ? 0 : 2;
+                else if (up > a.units)
+                    a.status[b] = 2;
+            }
+            before = __shfl(up, kWave - 1, kWave);
         }
     }
     // the rows that see most come first

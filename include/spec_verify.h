@@ -593,7 +593,8 @@ sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, lon
  *   req_status [B] optional: 0; 1 a token of the request sees a slot outside the table
  *     (or base[b] < 0), or a page outside the cache: the rows that see it are 0, their
  *     lse -inf, the rows before them as without it; 2 the request's bounds in starts are
- *     malformed (its rows are not written).
+ *     malformed (its rows are not written), or overlapping requests hold so many rows
+ *     that its own are not all reached.
  * Weights enter the second product rounded to bf16; sums and references are fp32.
  * Scores (scale q.k) must lie within +-1e29 and q.k within fp32.  What a masked slot
  * holds, infinities and NaN included, reaches no row.

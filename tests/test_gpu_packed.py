@@ -116,6 +116,21 @@ def test_bad_pages_tables_and_bounds(kind):
     check_attend(g, o, 100)
 
 
+def test_overlapping_bounds_all_have_a_status():
+    """Five requests of 128 tokens over the same 128, four rows a token: 20 row tiles where
+    the sizes allow 4 + 9.  The first three fit."""
+    note("packed overlap")
+    rng = np.random.default_rng(29)
+    cache = Cache(rng, 72, 1, 16, 64, "bf16")
+    table = np.arange(72).reshape(9, 8)
+    starts = np.array([0, 128] * 5)
+    full = torch.full((9,), 7, dtype=torch.int32, device=dev())
+    del full
+    q = torch.zeros(128, 4, 64, dtype=torch.bfloat16, device=dev())
+    g = sv.spec_attend_packed(q, cache.upload(), ints_to_dev(table), ints_to_dev(starts))
+    assert g["status"].tolist() == [0, 2, 0, 2, 0, 2, 2, 2, 2]
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_masked_slots_that_are_not_finite_reach_no_row(kind, D):
