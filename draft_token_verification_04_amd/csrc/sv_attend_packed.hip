@@ -142,9 +142,10 @@ struct Unit {
     int b, tile, first, count, base;  // request, its tile, first token, tokens, and cached ones before
     bool last;                        // the request's last tile
 };
-// Row tiles of a request of `count` tokens.
-__device__ __forceinline__ int tiles_of(int count, int G, int rows) {
-    return static_cast<int>((static_cast<long long>(count) * G + rows - 1) / rows);
+// Row tiles of a request of `count` tokens, or one more than the launch has if that is
+// less (so that 64 requests' sum fits).
+__device__ __forceinline__ int tiles_of(const PackedArgs &a, int count, int rows) {
+    return static_cast<int>(min((static_cast<long long>(count) * a.G + rows - 1) / rows, a.units + 1LL));
 }
 // Tokens of request i, 0 where its bounds are malformed.
 __device__ __forceinline__ int request_tokens(const PackedArgs &a, int i, int *first) {
@@ -152,15 +153,16 @@ __device__ __forceinline__ int request_tokens(const PackedArgs &a, int i, int *f
     *first = lo;
     return lo >= 0 && hi >= lo && hi <= a.T ? hi - lo : 0;
 }
-// The sum over the wave's lanes up to this one.
-__device__ __forceinline__ long long running_sum(int mine, int lane) {
-    long long up = mine;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const long long y = __shfl_up(up, o, kWave);
-        if (lane >= o) up += y;
-    }
-    return up;
+// The sum over the wave's lanes up to this one: within rows of 16 lanes, then the rows'
+// last lanes to the rows behind.
+__device__ __forceinline__ int running_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15, 31
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+    return v;
 }
 // The u-th row tile, requests in order, or b = -1 behind the last.  A wave sums the
 // tiles of 64 requests at a time.
@@ -172,8 +174,7 @@ __device__ __forceinline__ Unit find_unit(const PackedArgs &a, int u, int rows, 
             count = request_tokens(a, i0 + lane, &first);
             if (a.base) base = a.base[i0 + lane];
         }
-        const int mine = tiles_of(count, a.G, rows);
-        const long long up = running_sum(mine, lane);
+        const int mine = tiles_of(a, count, rows), up = running_sum(mine);
         const uint64_t past = __ballot(before + up > u);
         if (past) {
             const int at = __ffsll(static_cast<long long>(past)) - 1;
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(WAVES *kWave, D > 128 ? 1 : 2) void k_attend_packed
             const int b = i0 + lane;
             int first = 0;
             const int count = b < a.B ? request_tokens(a, b, &first) : 0;
-            const long long up = before + running_sum(tiles_of(count, a.G, kRows), lane);
+            const long long up = before + running_sum(tiles_of(a, count, kRows));
             if (b < a.B) {
                 if (count == 0)
                     a.status[b] = first == a.starts[b + 1] && first >= 0 && first <= a.T ? 0 : 2;
@@ -782,11 +783,26 @@ PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size
     p.units = static_cast<int>(std::max(1LL, std::min(all / p.rows + B, all)));
     const long long tiles = (static_cast<long long>(P) * page_size + kSlots - 1) / kSlots;
     const long long groups = static_cast<long long>(p.units) * Hkv;
-    // two workgroups of four waves, or one of eight, for each compute unit
-    long long S = std::max(1LL, kCus * (eight ? 1 : 2) / std::max(1LL, groups));
-    S = std::min(S, std::max(1LL, tiles / kLeastRun));
     const size_t per = static_cast<size_t>(groups) * p.rows * (D + 2) * 4;
-    while (S > 1 && per * S > (size_t{512} << 20)) --S;
+    // The least estimate of a row tile that sees the whole table, us: a tile of slots takes
+    // `alone` while every workgroup has a compute unit to itself, `shared` where two have
+    // one (with heads of 256 they follow one another), the join a launch and its traffic.
+    // 1000 tokens over 8 heads of 128: 30 us in one part, 39 in two; 100 over 8000 42 in
+    // eight, 46 in sixteen; 256 over 16000 122 in three, 105 in seven; 200 over 8000 with
+    // heads of 256 66 in nine, 85 in eighteen.
+    constexpr double kJoin = 5.0, kJoinBytes = 3e6;
+    const double size = D == 64 ? 0.75 : (D == 128 ? 1.0 : 2.5);
+    const double alone = size * (e4m3 ? 1.95 : 1.25), shared = D == 256 ? 2 * alone : size * (e4m3 ? 3.0 : 2.2);
+    const long long most = std::min(kCus * (eight ? 1 : 2) / std::max(1LL, groups), tiles / kLeastRun);
+    long long S = 1;
+    double best = 0;
+    for (long long n = 1; n <= std::max(1LL, most); ++n) {
+        if (n > 1 && per * n > (size_t{512} << 20)) break;
+        const double us = static_cast<double>((tiles + n - 1) / n) * (groups * n <= kCus ? alone : shared) + (n > 1 ? kJoin + per * n / kJoinBytes : 0.0);
+        if (best != 0 && us >= best) continue;
+        best = us;
+        S = n;
+    }
     p.S = static_cast<int>(S);
     if (S > 1) {
         size_t o = 0;
