@@ -220,7 +220,7 @@ def _check(t, name, ndim=None, dtype=None, device=None):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(torch, device, stream):
@@ -693,7 +693,7 @@ def _window_ints(torch, t, name, shape, dev):
     if t is None:
         return
     _check(t, name, len(shape), torch.int32, dev)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
 
 
@@ -701,7 +701,7 @@ def _window_out(torch, t, name, shape, dtype, dev):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     _check(t, name, len(shape), dtype, dev)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
     return t
 
@@ -894,7 +894,7 @@ def _matrix(torch, t, name, dtype, dev=None, shape=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
@@ -923,14 +923,16 @@ def spec_rms_norm(x, weight=None, *, eps=1e-6, residual=None, residual_out=None,
     res = {}
     if residual is not None:
         _check(residual, "residual", 2, torch.bfloat16, dev)
-        if tuple(residual.shape) != (T, D):
+        if residual.shape != (T, D):
             raise ValueError(f"residual must be [{T}, {D}]")
-        res["residual"] = _window_out(torch, residual_out, "residual_out", (T, D), torch.bfloat16, dev)
+        res["residual"] = (residual.new_empty((T, D)) if residual_out is None else
+                           _window_out(torch, residual_out, "residual_out", (T, D), torch.bfloat16, dev))
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    res["out"] = _window_out(torch, out, "out", (T, D), torch.float8_e4m3fn if e4m3 else torch.bfloat16, dev)
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    res["out"] = x.new_empty((T, D), dtype=dt) if out is None else _window_out(torch, out, "out", (T, D), dt, dev)
     if e4m3:
-        res["scales"] = torch.empty((-(-D // SCALE_BLOCK), T), dtype=torch.float32, device=dev)
+        res["scales"] = x.new_empty((-(-D // SCALE_BLOCK), T), dtype=torch.float32)
     rc = _call(torch, lib.spec_rms_norm, dev, stream, x.data_ptr(), xs, _ptr(residual), _ptr(weight), float(eps), T, D,
                _ptr(res.get("residual")), res["out"].data_ptr(), SV_E4M3 if e4m3 else SV_BF16, _ptr(res.get("scales")))
     if rc != SV_OK:
@@ -963,7 +965,7 @@ def spec_linear_e4m3(x, x_scales, w, w_scales, *, out=None, out_dtype=None, work
         raise ValueError(f"w must be [N, {K}], got {list(w.shape)}")
     ss = _matrix(torch, x_scales, "x_scales", torch.float32, dev, (blocks, M))
     _check(w_scales, "w_scales", 2, torch.float32, dev)
-    if tuple(w_scales.shape) != (-(-N // SCALE_BLOCK), blocks):
+    if w_scales.shape != (-(-N // SCALE_BLOCK), blocks):
         raise ValueError(f"w_scales must be [{-(-N // SCALE_BLOCK)}, {blocks}]")
     if out is not None:
         out_dtype = out.dtype
@@ -971,7 +973,7 @@ def spec_linear_e4m3(x, x_scales, w, w_scales, *, out=None, out_dtype=None, work
         out_dtype = torch.bfloat16
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out must be bfloat16 or float32, got {out_dtype}")
-    out = _window_out(torch, out, "out", (M, N), out_dtype, dev)
+    out = x.new_empty((M, N), dtype=out_dtype) if out is None else _window_out(torch, out, "out", (M, N), out_dtype, dev)
     dt = SV_F32 if out_dtype == torch.float32 else SV_BF16
     ws = _workspace(torch, linear_workspace_bytes(M, N, K, dt), dev, workspace)
     rc = _call(torch, lib.spec_linear_e4m3, dev, stream, x.data_ptr(), xs, x_scales.data_ptr(), ss, w.data_ptr(),
