@@ -933,7 +933,7 @@ bool stride_ok(long long stride, long long least, bool several) {
 
 bool packed_sizes_ok(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size, bool e4m3) {
     if (!paged_sizes_ok(page_size, head_dim) || static_cast<long long>(P) * page_size > kMaxSlots) return false;
-    if (H > 65536 || static_cast<double>(T) * H > 2.0e9) return false;
+    if (H > 65536 || static_cast<double>(T) * H > 2.0e9 || B > kMaxGroups) return false;
     if (B == 0) return true;
     const PackedPlan p = packed_plan(T, B, H, kv_heads, head_dim, P, page_size, e4m3);
     return packed_groups(kv_heads, p) <= kMaxGroups && packed_join_groups(kv_heads, head_dim, p) <= kMaxGroups;

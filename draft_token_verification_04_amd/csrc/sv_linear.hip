@@ -539,7 +539,7 @@ size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 template <typename S>
 long long tiles_of(int M, int N) {
-    return static_cast<long long>((M + S::kTokens - 1) / S::kTokens) * ((N + S::kWRows - 1) / S::kWRows);
+    return ((M + S::kTokens - 1LL) / S::kTokens) * ((N + S::kWRows - 1LL) / S::kWRows);
 }
 long long whole_xcds(long long tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
 template <typename S, bool F32>
@@ -587,7 +587,7 @@ LinearPlan linear_plan(int M, int N, int K, bool f32) {
     const int blocks = (K + kScaleBlock - 1) / kScaleBlock;
     if (M <= 16 || (M <= kFewTokens && N <= kFewManyRows)) {
         p.kind = kFew;
-        p.groups = (N + 15) / 16;
+        p.groups = (N + 15LL) / 16;
         return p;
     }
     const Cost costs[3] = {{kSmall, f32 ? 0.82 : 0.58, f32 ? 0.60 : 0.37, tiles_of<SmallShape>(M, N)},

@@ -124,6 +124,18 @@ def test_attend_packed_refusals(lib):
     assert f(64, 64, 64, 64, 256, 1 << 20, 16, sv.SV_BF16) <= 513 << 20
 
 
+def test_the_largest_sizes_are_refused(lib):
+    top = (1 << 31) - 1
+    f = lib.sv_linear_workspace_bytes
+    for m, n in [(1, top), (17, top), (64, top), (top, 1), (top, 64), (top, top), (300, top), (top - 300, 1), (1, top - 15)]:
+        for dt in (sv.SV_BF16, sv.SV_F32):
+            assert f(m, n, 16, dt) == 0, (m, n, dt)
+            assert _linear(lib, M=m, N=n, K=16, ss=1 << 31, dt=dt) == UNS, (m, n, dt)
+    f = lib.sv_attend_packed_workspace_bytes
+    for t, b in [(7, top), (0, top), (7, top - 63), (7, 1 << 24), (top, 1), (top, top)]:
+        assert f(t, b, 4, 2, 128, 5, 16, sv.SV_BF16) == 0 and _attend(lib, T=t, B=b, wsb=1 << 40) == UNS, (t, b)
+
+
 def test_constants_match_the_header():
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                              "spec_verify.h")).read()
