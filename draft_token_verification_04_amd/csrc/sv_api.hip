@@ -1025,7 +1025,7 @@ sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, lon
         if (rot < 1 || rot > D || max_pos < 1 || axes < 1 || (axes > 1 && !pair_axis)) return SV_ERR_INVALID_ARG;
         if (rot % 16 != 0 || axes > SV_MAX_AXES) return SV_ERR_UNSUPPORTED;
     }
-    if (T > kMaxGroups || static_cast<long long>(H) + 2LL * cache.kv_heads > 65536 || B == 0x7fffffff)
+    if (T > kMaxGroups || static_cast<long long>(H) + 2LL * cache.kv_heads > 65536 || B > kMaxGroups)
         return SV_ERR_UNSUPPORTED;
     if (T == 0) return SV_OK;
     if (!q || !k || !v || !starts || (B > 0 && !page_table) || !q_out || (rope && !positions)) return SV_ERR_INVALID_ARG;

@@ -557,7 +557,7 @@ sv_status spec_linear_e4m3(const void *x, long long x_stride, const float *x_sca
  *   starts [B + 1] int32, rising: the tokens of request b are starts[b] ...
  *     starts[b + 1] - 1, none where the two are equal.  Tokens outside every request
  *     write nothing.  starts that do not rise give unspecified rows (none is read or
- *     written outside the arrays).
+ *     written outside the arrays).  B below 2^24 (else SV_ERR_UNSUPPORTED).
  *   base [B] int32: the request's cached tokens before these, or NULL (none).  Token
  *     starts[b] + j takes slot base[b] + j.
  *   positions [axes][T] int32, 1 <= axes <= SV_MAX_AXES (images and video have positions

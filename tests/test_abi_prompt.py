@@ -131,6 +131,8 @@ def test_the_largest_sizes_are_refused(lib):
         for dt in (sv.SV_BF16, sv.SV_F32):
             assert f(m, n, 16, dt) == 0, (m, n, dt)
             assert _linear(lib, M=m, N=n, K=16, ss=1 << 31, dt=dt) == UNS, (m, n, dt)
+    for b in (top - 1, top - 63, 1 << 24):
+        assert _append(lib, B=b) == UNS, b
     f = lib.sv_attend_packed_workspace_bytes
     for t, b in [(7, top), (0, top), (7, top - 63), (7, 1 << 24), (top, 1), (top, top)]:
         assert f(t, b, 4, 2, 128, 5, 16, sv.SV_BF16) == 0 and _attend(lib, T=t, B=b, wsb=1 << 40) == UNS, (t, b)
