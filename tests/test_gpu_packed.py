@@ -71,6 +71,22 @@ def test_chunks_over_long_contexts_are_split_and_joined(kind):
     check_attend(g, o, 9040)
 
 
+@pytest.mark.parametrize("kind,H,Hkv", [("bf16", 4, 2), ("e4m3", 4, 2), ("bf16", 130, 1), ("bf16", 300, 2)])
+def test_many_requests_and_many_heads_of_one(kind, H, Hkv):
+    # more requests than a wave holds at a time; row tiles that begin inside a token
+    note(f"packed requests {kind} H={H}")
+    rng = np.random.default_rng(H)
+    n = rng.integers(0, 5, 150)
+    n[130] = 70
+    base = rng.integers(0, 60, 150)
+    starts = np.concatenate([[0], np.cumsum(n)])
+    table, pages = _table(rng, 150, 9)
+    cache = Cache(rng, pages, Hkv, 16, 64, kind)
+    g, o = run_packed(rng, cache, table, starts, base, int(starts[-1]), H)
+    assert (o["status"] == 0).all()
+    check_attend(g, o, 150)
+
+
 def test_without_base_and_at_the_first_token():
     note("packed no base")
     rng = np.random.default_rng(4)
