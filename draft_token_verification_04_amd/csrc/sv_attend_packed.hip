@@ -779,8 +779,9 @@ PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size
     const long long all = static_cast<long long>(T) * (H / Hkv);
     const bool eight = eight_waves(all, Hkv, D, e4m3);
     p.rows = eight ? 256 : 128;
-    // every request may end in a part of a tile; none has more tiles than rows
-    p.units = static_cast<int>(std::max(1LL, std::min(all / p.rows + B, all)));
+    // every request may end in a part of a tile (of one row at least); none has more tiles
+    // than rows
+    p.units = static_cast<int>(std::max(1LL, std::min((all + B * (p.rows - 1LL)) / p.rows, all)));
     const long long tiles = (static_cast<long long>(P) * page_size + kSlots - 1) / kSlots;
     const long long groups = static_cast<long long>(p.units) * Hkv;
     const size_t per = static_cast<size_t>(groups) * p.rows * (D + 2) * 4;
