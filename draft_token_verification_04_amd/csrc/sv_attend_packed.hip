@@ -760,6 +760,43 @@ hipError_t launch_d(const PackedArgs &a, bool e4m3, const PackedPlan &p, hipStre
     return e4m3 ? launch_waves<D, true>(a, p, s) : launch_waves<D, false>(a, p, s);
 }
 
+constexpr long long kCus = 256;
+
+// Row tiles of `rows` rows and the parts of their slots, with an estimate of a launch.
+struct Parts {
+    long long units, groups, S;
+    double us;
+};
+
+// The parts with the least estimate of a row tile that sees the whole table, us: a tile of
+// slots takes `alone` while every workgroup has a compute unit to itself, `shared` where two
+// have one (with heads of 256 they follow one another; eight waves have one alone), the
+// join a launch and its traffic.  1000 tokens over 8 heads of 128: 30 us in one part, 39 in
+// two; 100 over 8000 42 in eight, 46 in sixteen; 256 over 16000 122 in three, 105 in seven;
+// 200 over 8000 with heads of 256 66 in nine, 85 in eighteen.
+Parts parts_of(long long all, int B, int Hkv, int D, long long tiles, int rows, bool e4m3) {
+    constexpr double kJoin = 5.0, kJoinBytes = 3e6, kEightMore = 3.0;
+    const bool eight = rows == 256;
+    const double size = D == 64 ? 0.75 : (D == 128 ? 1.0 : 2.5);
+    const double alone = size * (eight ? 2.3 : (e4m3 ? 1.95 : 1.25));
+    const double shared = D == 256 ? 2 * alone : size * (e4m3 ? 2.7 : 2.2);
+    Parts p = {};
+    // every request may end in a part of a tile (of one row at least); none has more tiles
+    // than rows
+    p.units = std::max(1LL, std::min((all + B * (rows - 1LL)) / rows, all));
+    p.groups = p.units * Hkv;
+    const double bytes = static_cast<double>(p.groups) * rows * (D + 2) * 4;
+    const long long most = std::min(kCus * (eight ? 1 : 2) / p.groups, tiles / kLeastRun);
+    for (long long n = 1; n <= std::max(1LL, most) && (n == 1 || bytes * n <= 512 << 20); ++n) {
+        const double us = static_cast<double>((tiles + n - 1) / n) * (p.groups * n <= kCus ? alone : shared) +
+                          (n > 1 ? kJoin + bytes * n / kJoinBytes : 0.0) + (eight ? kEightMore : 0.0);
+        if (n > 1 && us >= p.us) continue;
+        p.us = us;
+        p.S = n;
+    }
+    return p;
+}
+
 }  // namespace
 
 long long packed_groups(int Hkv, const PackedPlan &p) { return static_cast<long long>(p.units) * Hkv * p.S; }
@@ -768,51 +805,35 @@ long long packed_join_groups(int Hkv, int D, const PackedPlan &p) {
     return p.S == 1 ? 0 : static_cast<long long>(p.units) * Hkv * (p.rows / (kBlock / (D / 4)));
 }
 
-// An e4m3 cache's rows are widened once by each workgroup, so with heads of 128 eight
-// waves share them where the rows fill the card (512 tokens over 16000: 190 us, and 203
-// with four; heads of 64 leave eight waves less than a load each, 256 one wave a SIMD).
-constexpr long long kCus = 256;
-bool eight_waves(long long rows, int Hkv, int D, bool e4m3) { return e4m3 && D == 128 && rows * Hkv >= kCus * 64; }
-
 PackedPlan packed_plan(int T, int B, int H, int Hkv, int D, int P, int page_size, bool e4m3) {
-    PackedPlan p = {};
     const long long all = static_cast<long long>(T) * (H / Hkv);
-    const bool eight = eight_waves(all, Hkv, D, e4m3);
-    p.rows = eight ? 256 : 128;
-    // every request may end in a part of a tile (of one row at least); none has more tiles
-    // than rows
-    p.units = static_cast<int>(std::max(1LL, std::min((all + B * (p.rows - 1LL)) / p.rows, all)));
     const long long tiles = (static_cast<long long>(P) * page_size + kSlots - 1) / kSlots;
-    const long long groups = static_cast<long long>(p.units) * Hkv;
-    const size_t per = static_cast<size_t>(groups) * p.rows * (D + 2) * 4;
-    // The least estimate of a row tile that sees the whole table, us: a tile of slots takes
-    // `alone` while every workgroup has a compute unit to itself, `shared` where two have
-    // one (with heads of 256 they follow one another), the join a launch and its traffic.
-    // 1000 tokens over 8 heads of 128: 30 us in one part, 39 in two; 100 over 8000 42 in
-    // eight, 46 in sixteen; 256 over 16000 122 in three, 105 in seven; 200 over 8000 with
-    // heads of 256 66 in nine, 85 in eighteen.
-    constexpr double kJoin = 5.0, kJoinBytes = 3e6;
-    const double size = D == 64 ? 0.75 : (D == 128 ? 1.0 : 2.5);
-    const double alone = size * (e4m3 ? 1.95 : 1.25), shared = D == 256 ? 2 * alone : size * (e4m3 ? 3.0 : 2.2);
-    const long long most = std::min(kCus * (eight ? 1 : 2) / std::max(1LL, groups), tiles / kLeastRun);
-    long long S = 1;
-    double best = 0;
-    for (long long n = 1; n <= std::max(1LL, most); ++n) {
-        if (n > 1 && per * n > (size_t{512} << 20)) break;
-        const double us = static_cast<double>((tiles + n - 1) / n) * (groups * n <= kCus ? alone : shared) + (n > 1 ? kJoin + per * n / kJoinBytes : 0.0);
-        if (best != 0 && us >= best) continue;
-        best = us;
-        S = n;
+    PackedPlan p = {};
+    p.rows = 128;
+    Parts use = parts_of(all, B, Hkv, D, tiles, 128, e4m3);
+    // An e4m3 cache's rows are widened by each workgroup, so with heads of 128 eight waves
+    // share them where there are row tiles for many rounds, or parts that fill the card
+    // (8191 tokens: 605 us, 628 with four; 512 over 16000 188 and 197; but 2000 tokens 73 and
+    // 64, as a tile's slots are all one workgroup's.  Heads of 64 leave eight waves less
+    // than a load each, 256 one wave a SIMD).
+    if (e4m3 && D == 128) {
+        const Parts eight = parts_of(all, B, Hkv, D, tiles, 256, e4m3);
+        if (use.groups >= 4 * kCus || (eight.S > 1 && eight.us < use.us)) {
+            p.rows = 256;
+            use = eight;
+        }
     }
-    p.S = static_cast<int>(S);
-    if (S > 1) {
+    p.units = static_cast<int>(use.units);
+    p.S = static_cast<int>(use.S);
+    if (p.S > 1) {
+        const size_t parts = static_cast<size_t>(use.groups) * p.S;
         size_t o = 0;
         p.part_o = o;
-        o = align_up(o + static_cast<size_t>(groups) * S * p.rows * D * 4);
+        o = align_up(o + parts * p.rows * D * 4);
         p.part_ml = o;
-        o = align_up(o + static_cast<size_t>(groups) * S * p.rows * 2 * 4);
+        o = align_up(o + parts * p.rows * 2 * 4);
         p.part_bad = o;
-        o = align_up(o + static_cast<size_t>(groups) * S * 4);
+        o = align_up(o + parts * 4);
         p.total = o;
     }
     return p;

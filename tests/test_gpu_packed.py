@@ -87,6 +87,24 @@ def test_many_requests_and_many_heads_of_one(kind, H, Hkv):
     check_attend(g, o, 150)
 
 
+def test_e4m3_rows_shared_by_eight_waves():
+    # many row tiles of 256 rows, most of them partly filled; then parts of a long context
+    note("packed eight waves")
+    rng = np.random.default_rng(31)
+    n, base = rng.integers(1, 20, 64), rng.integers(0, 40, 64)
+    n[[5, 40]], base[[5, 40]] = [300, 257], [400, 3]
+    starts = np.concatenate([[0], np.cumsum(n)])
+    table, pages = _table(rng, 64, 22)
+    cache = Cache(rng, pages, 16, 32, 128, "e4m3")
+    g, o = run_packed(rng, cache, table, starts, base, int(starts[-1]), 16)
+    check_attend(g, o, 700)
+    table, pages = _table(rng, 1, 516)
+    cache = Cache(rng, pages, 8, 32, 128, "e4m3")
+    assert sv.attend_packed_workspace_bytes(500, 1, 8, 8, 128, 516, 32, sv.SV_E4M3) > 256
+    g, o = run_packed(rng, cache, table, [0, 500], [16000], 500, 8)
+    check_attend(g, o, 16500)
+
+
 def test_without_base_and_at_the_first_token():
     note("packed no base")
     rng = np.random.default_rng(4)
