@@ -569,14 +569,16 @@ enum { kFew = 0, kSmall = 1, kMid = 2, kBig = 3 };
 constexpr int kFewTokens = 32, kFewManyRows = 8192;
 
 // Tiles: the shape and the parts of K with the least estimate of
-//   steps * max(alone, tiles per compute unit * step) + join.
-// `alone` is what a block of 128 takes a single workgroup on its compute unit, `step`
-// what it adds where there are several (us; from 256 x 4096 x 12288 and 8191 x 24576 x
-// 4096, fp32 2048 x 151936 x 4096).  The estimate is within 15% of the measured time at
-// 128 to 8191 tokens.
+//   steps * max(alone, rounds * step) + max(1, rounds) * ends + join,
+// rounds the tiles for each compute unit.  `alone` is what a block of 128 takes a single
+// workgroup on its compute unit, `step` what it adds where there are several, `ends` a
+// tile's first loads and its stores (us; from 128 to 8191 tokens, 2000 to 151936 rows of W).
+// Of 26 sizes measured in every shape and number of parts the choice is within 8% of the
+// best, but for two at 14% (100 x 4096 x 12288: 64 x 128 tiles in eight parts 19 us, 128 x
+// 128 26; 3000 x 4096 x 12288: 256 x 256 187 us, 128 x 128 194).
 struct Cost {
     int kind;
-    double alone, step;
+    double alone, step, ends;
     long long tiles;
 };
 constexpr double kCus = 256;
@@ -590,9 +592,9 @@ LinearPlan linear_plan(int M, int N, int K, bool f32) {
         p.groups = (N + 15LL) / 16;
         return p;
     }
-    const Cost costs[3] = {{kSmall, f32 ? 0.82 : 0.58, f32 ? 0.60 : 0.37, tiles_of<SmallShape>(M, N)},
-                           {kMid, f32 ? 1.1 : 0.70, f32 ? 1.15 : 0.61, tiles_of<MidShape>(M, N)},
-                           {kBig, f32 ? 1.9 : 1.85, f32 ? 2.15 : 1.9,
+    const Cost costs[3] = {{kSmall, f32 ? 0.82 : 0.58, f32 ? 0.60 : 0.37, 1.0, tiles_of<SmallShape>(M, N)},
+                           {kMid, f32 ? 1.1 : 0.70, f32 ? 1.15 : 0.61, 3.0, tiles_of<MidShape>(M, N)},
+                           {kBig, f32 ? 1.9 : 1.8, f32 ? 2.15 : 1.8, 6.0,
                             f32 ? tiles_of<BigShapeWide>(M, N) : tiles_of<BigShape>(M, N)}};
     double best = 0;
     for (const Cost &c : costs) {
@@ -602,7 +604,8 @@ LinearPlan linear_plan(int M, int N, int K, bool f32) {
             // the largest tile has its compute unit to itself: whole rounds
             const double per = c.tiles * splits / kCus, rounds = c.kind == kBig ? ceil(per) : per;
             const double steps = static_cast<double>((blocks + splits - 1) / splits);
-            const double us = steps * std::max(c.alone, rounds * c.step) + (splits > 1 ? 3.5 + bytes / 5e6 : 0.0);
+            const double us = steps * std::max(c.alone, rounds * c.step) + std::max(1.0, rounds) * c.ends +
+                              (splits > 1 ? 5.0 + bytes / 5e6 : 0.0);
             if (best != 0 && us >= best) continue;
             best = us;
             p.kind = c.kind;
