@@ -28,6 +28,18 @@ def test_sizes(M, N, K, dtype):
 @DTYPES
 def test_shapes_of_each_kernel(M, N, K, dtype):
     note(f"linear M={M} N={N} K={K} {dtype}")
+    _exact(M, N, K, dtype)
+
+
+# one row of tiles over many rows of W, 128 x 128 and the largest
+@pytest.mark.parametrize("M,N", [(128, 33000), (250, 65500)])
+@DTYPES
+def test_one_row_of_the_larger_tiles(M, N, dtype):
+    note(f"linear one row of tiles {M} {dtype}")
+    _exact(M, N, 4000, dtype)
+
+
+def _exact(M, N, K, dtype):
     c = LinearCase(np.random.default_rng(N), M, N, K, exact=True)
     out = sv.spec_linear_e4m3(*c.upload(), out_dtype=dtype)
     x, xs, w, ws = c.upload()
@@ -36,6 +48,16 @@ def test_shapes_of_each_kernel(M, N, K, dtype):
     wd = w.double() * ws.double().repeat_interleave(128, 0)[:N][:, column]
     want = (xd @ wd.t()).to(torch.float32)  # exact: whole multiples of 1/4 far below 2^22
     assert torch.equal(out, want.to(dtype))
+
+
+@DTYPES
+@pytest.mark.parametrize("M", [1000, 2000])
+def test_long_sums_in_the_larger_tiles(M, dtype):
+    # tiles of 128 x 128, and of 256 x 128 for fp32 where there are twice the tokens
+    note(f"linear larger tiles {M} {dtype}")
+    rng = np.random.default_rng(M)
+    c = LinearCase(rng, M, 4090, 4000)
+    c.check(sv.spec_linear_e4m3(*c.upload(), out_dtype=dtype))
 
 
 @DTYPES
