@@ -40,17 +40,23 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v + __shfl_xor(v, 32, kWave);
 }
 
+// A row whose mean square and eps overflow together, or are below kLeastMean together
+// (the squares that underflow are 2^-150 off each), is scaled by kFar down or up before it
+// is squared: its largest value is above 2^56 (or eps is), or below 2^-43, so scaled
+// squares neither overflow nor lose what counts.
+constexpr float kLeastMean = 0x1p-100f, kFar = 0x1p80f;
+
 template <int TPR, int V, bool E4M3>
 __global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void k_rms_norm(NormArgs a) {
     constexpr int kThreads = TPR > kBlock ? TPR : kBlock;
     constexpr int kRows = kThreads / TPR, kWaves = TPR / kWave;
+    static_assert(kWaves == 1 || kRows == 1, "rows of several waves have a workgroup each");
     __shared__ float sums[kThreads / kWave];
     const int l = threadIdx.x % TPR;
     const int t = blockIdx.x * kRows + static_cast<int>(threadIdx.x) / TPR;
     const bool live = t < a.T;
     const long long row = static_cast<long long>(live ? t : 0) * a.D;
     float h[V][8];
-    float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int d = (i * TPR + l) * 8;
@@ -70,20 +76,35 @@ __global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void k_rms_norm(NormAr
             }
         }
     }
+    // the mean of the row's squares, its values times `by` first; the same in all its lanes
+    auto mean_square = [&](float by) {
+        float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += h[i][e] * h[i][e];
-    ss = wave_sum(ss);
-    if constexpr (kWaves > 1) {
-        sums[threadIdx.x / kWave] = ss;
-        __syncthreads();
-        const int w0 = threadIdx.x / TPR * kWaves;
-        ss = 0.0f;
+            for (int e = 0; e < 8; ++e) {
+                const float v = h[i][e] * by;
+                ss += v * v;
+            }
+        ss = wave_sum(ss);
+        if constexpr (kWaves > 1) {
+            sums[threadIdx.x / kWave] = ss;
+            __syncthreads();
+            ss = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) ss += sums[w0 + w];
+            for (int w = 0; w < kWaves; ++w) ss += sums[w];
+        }
+        return ss / static_cast<float>(a.D);
+    };
+    float mean = mean_square(1.0f), eps = a.eps, up = 1.0f, down = 1.0f;
+    const bool over = isinf(mean + eps);
+    if (over || mean + eps < kLeastMean) {  // the same in all lanes of a row
+        if constexpr (kWaves > 1) __syncthreads();  // the sums before have been read
+        (over ? down : up) = over ? 1.0f / kFar : kFar;
+        mean = mean_square(up * down);
+        eps = eps * up * down * up * down;
     }
-    const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.D) + a.eps);
+    const float inv = 1.0f / sqrtf(mean + eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int d = (i * TPR + l) * 8;
@@ -94,7 +115,7 @@ __global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void k_rms_norm(NormAr
                            pack_bf16(h[i][6], h[i][7]));
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * inv;
+        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * up * inv * down;
         if (a.weight && in) {
             float w[8];
             unpack(*reinterpret_cast<const uint4 *>(a.weight + d), w);

@@ -518,9 +518,10 @@ sv_status spec_token_logprobs(const void *logits, const int32_t *tokens, int R, 
  *     a = max |y| over them (zeros: scale 0).
  *   D a multiple of 8, at most SV_MAX_NORM_COLS (else SV_ERR_UNSUPPORTED); everything
  *   16-byte aligned.  out must not overlap the inputs.
- * Computed in fp32 from h as added, and rounded once, to nearest even (h^2 included:
- * |h| up to 1e18).  A row that holds an infinity or NaN has no finite norm: what it
- * gives is NaN where y is.
+ * Computed in fp32 from h as added, and rounded once, to nearest even.  h may be of any
+ * finite size: a row whose squares would leave fp32's range is scaled by a power of two
+ * first.  A row of zeros with eps = 0 gives NaN (0 / 0).  A row that holds an infinity or
+ * NaN has no finite norm: what it gives is NaN where y is.
  */
 sv_status spec_rms_norm(const void *x, long long x_stride, const void *residual, const void *weight, float eps, int T,
                         int D, void *residual_out, void *out, sv_dtype out_dt, float *out_scale, hipStream_t stream);
