@@ -936,7 +936,9 @@ bool packed_sizes_ok(int T, int B, int H, int kv_heads, int head_dim, int P, int
     if (H > 65536 || static_cast<double>(T) * H > 2.0e9 || B > kMaxGroups) return false;
     if (B == 0) return true;
     const PackedPlan p = packed_plan(T, B, H, kv_heads, head_dim, P, page_size, e4m3);
-    return packed_groups(kv_heads, p) <= kMaxGroups && packed_join_groups(kv_heads, head_dim, p) <= kMaxGroups;
+    // 128 rows take a workgroup of 256 work items, 256 rows one of 512
+    return packed_groups(kv_heads, p) * (p.rows / 128) <= kMaxGroups &&
+           packed_join_groups(kv_heads, head_dim, p) <= kMaxGroups;
 }
 
 }  // namespace

@@ -61,7 +61,7 @@ struct PackedArgs {
     int32_t *part_bad;        // [units][Hkv][S]
 };
 struct PackedPlan {
-    int rows;           // rows of a workgroup
+    int rows;           // rows of a workgroup, two work items each
     int units, S;
     size_t part_o, part_ml, part_bad, total;
 };

@@ -607,7 +607,9 @@ sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, lon
  * Scores (scale q.k) must lie within +-1e29 and q.k within fp32.  What a masked slot
  * holds, infinities and NaN included, reaches no row.
  * Workspace: sv_attend_packed_workspace_bytes (0 for invalid or unsupported sizes), at
- * most about 512 MB.
+ * most about 512 MB.  Sizes whose launch would have 2^32 work items are unsupported: 2^24
+ * workgroups of 128 rows (tokens x query heads of a KV head), or for an e4m3 cache with
+ * heads of 128 half as many of 256; a request's last rows take one of their own.
  */
 size_t sv_attend_packed_workspace_bytes(int T, int B, int H, int kv_heads, int head_dim, int P, int page_size,
                                         sv_dtype cache_dt);
