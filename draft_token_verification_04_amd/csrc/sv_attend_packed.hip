@@ -256,7 +256,8 @@ __global__ __launch_bounds__(WAVES *kWave, D > 128 ? 1 : 2) void k_attend_packed
     const bool inside = base >= 0;
     const int total = inside ? static_cast<int>(min(want, exist)) : 0;
     const int least = inside ? static_cast<int>(min(static_cast<long long>(base) + r0 / a.G + 1, exist)) : 0;
-    int first_bad = inside ? (want > exist ? static_cast<int>(exist) : 0x7fffffff) : -0x7fffffff;
+    // the first slot that does not exist (before any row's last, where the base is negative)
+    int first_bad = inside ? (want > exist ? static_cast<int>(exist) : 0x7fffffff) : -0x7fffffff - 1;
 
     const int tiles = (total + kSlots - 1) / kSlots;
     const int active = splits_of(tiles, a.S);
