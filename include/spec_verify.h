@@ -604,8 +604,9 @@ sv_status spec_append_kv_packed(const void *q, const void *k, const void *v, lon
  *     malformed (its rows are not written), or overlapping requests hold so many rows
  *     that its own are not all reached.
  * Weights enter the second product rounded to bf16; sums and references are fp32.
- * Scores (scale q.k) must lie within +-1e29 and q.k within fp32.  What a masked slot
- * holds, infinities and NaN included, reaches no row.
+ * Scores (scale q.k) must lie within +-1e29, q.k within fp32 and values within +-2^90 (a
+ * row's weights sum to at most 2^8 times its slots).  What a masked slot holds, infinities
+ * and NaN included, reaches no row.
  * Workspace: sv_attend_packed_workspace_bytes (0 for invalid or unsupported sizes), at
  * most about 512 MB.  Sizes whose launch would have 2^32 work items are unsupported: 2^24
  * workgroups of 128 rows (tokens x query heads of a KV head), or for an e4m3 cache with
