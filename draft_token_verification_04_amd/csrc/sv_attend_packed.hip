@@ -774,7 +774,9 @@ struct Parts {
 // have one (with heads of 256 they follow one another; eight waves have one alone), the
 // join a launch and its traffic.  1000 tokens over 8 heads of 128: 30 us in one part, 39 in
 // two; 100 over 8000 42 in eight, 46 in sixteen; 256 over 16000 122 in three, 105 in seven;
-// 200 over 8000 with heads of 256 66 in nine, 85 in eighteen.
+// 200 over 8000 with heads of 256 66 in nine, 85 in eighteen.  The lengths are the device's,
+// so a table wider than its requests is planned for as if they filled it: 500 tokens take
+// 18 us in a table of 512 slots, and in one of 8192 19 and a join of 4 that has nothing to do.
 Parts parts_of(long long all, int B, int Hkv, int D, long long tiles, int rows, bool e4m3) {
     constexpr double kJoin = 5.0, kJoinBytes = 3e6, kEightMore = 3.0;
     const bool eight = rows == 256;
